@@ -372,12 +372,173 @@ LQ_API const char *lq_status_string(lq_status s);
                                       expired); the affected outputs are not
                                       valid */
 #define LQ_DEVERR_BAD_POSITION 2u  /* lq_decode_ragged / lq_ragged_flush met a
-                                      per-sequence position >= W and skipped
-                                      that sequence */
+                                      per-sequence position >= W, or a cache
+                                      or norm call a position past its table,
+                                      and skipped that sequence or token */
+#define LQ_DEVERR_BAD_PAGE 4u      /* a block_table entry outside the cache's
+                                      pages */
 
 /* Reads and clears the library's device error word, an OR of LQ_DEVERR_*
  * bits (synchronizes the device). */
 LQ_API lq_status lq_device_errors(uint32_t *flags);
+
+/* --------------------------------------------------------------------------
+ * Softmax-attention layers of a hybrid model
+ * --------------------------------------------------------------------------
+ * Models built on the recurrence above interleave linear-attention layers
+ * with softmax-attention layers, and normalise q and k per head in both.
+ * These calls serve what stands beside the recurrence in such a model: the
+ * per-head norm and position rotation of q and k, a paged key-value cache
+ * that new tokens are appended to, and attention over that cache for one new
+ * token per sequence (decode) or for runs of new tokens (prefill).
+ *
+ * A step of one layer is lq_kv_append followed by lq_attn_decode or
+ * lq_attn_prefill with the same `pos` array: pos[b] is the number of tokens
+ * sequence b had in the cache before the step (negative: idle slot).  The
+ * caller advances pos once all layers of the step are done.
+ *
+ * The conventions of the calls above hold: device memory is caller-owned,
+ * calls are asynchronous on `stream` and need the stream's device to be
+ * current, arguments are validated before anything is launched.  Values in
+ * device arrays (pos, cu_tokens, block_table, positions) cannot be validated
+ * on the host: the kernels check each one before they use it, skip the token
+ * or sequence concerned and record it in the device error word.  All sums,
+ * norms, angles and softmax statistics are FP32; outputs are rounded once to
+ * io_dtype. */
+
+/* Per-head norm of q and k.  LQ_NORM_L2: x / sqrt(sum x^2 + eps) (what the
+ * linear-attention calls expect of their q and k); LQ_NORM_RMS:
+ * x / sqrt(mean x^2 + eps).  Either is followed by a product with a weight
+ * per channel where one is given.  |x| must stay below 1e18 (the sum of
+ * squares is FP32). */
+typedef enum { LQ_NORM_NONE = 0, LQ_NORM_L2 = 1, LQ_NORM_RMS = 2 } lq_norm;
+
+/* Which channels of the first rot_dim form pair i (of rot_dim / 2):
+ * (i, i + rot_dim / 2) or (2 i, 2 i + 1). */
+typedef enum { LQ_ROT_HALVES = 0, LQ_ROT_ADJACENT = 1 } lq_rot_pairs;
+
+typedef struct {
+    int32_t q_heads;   /* Hq >= 1, a multiple of kv_heads; query head h reads
+                          key-value head h / (Hq / Hkv)                      */
+    int32_t kv_heads;  /* Hkv >= 1; Hq <= 4096                               */
+    int32_t head_dim;  /* D: 64, 128 or 256 (else LQ_ERR_UNSUPPORTED)        */
+    int32_t io_dtype;  /* lq_dtype of q, k, v, o and of the cache            */
+    int32_t norm;      /* lq_norm                                            */
+    int32_t rot_dim;   /* rotated channels: a multiple of 16 in [0, D]; 0: no
+                          rotation                                           */
+    int32_t rot_pairs; /* lq_rot_pairs                                       */
+    int32_t window;    /* > 0: a query sees itself and the window - 1 tokens
+                          before it; 0: all tokens before it                 */
+    float eps;         /* > 0 and finite (used with a norm)                  */
+    float scale;       /* factor of q . k; finite                            */
+    float softcap;     /* > 0: scores s become softcap tanh(s / softcap)
+                          before the mask; 0: off                            */
+} lq_attn_config;
+
+/* A paged key-value cache: pages of page_size tokens, a page holding all
+ * key-value heads, head-major:
+ *   k_pages, v_pages  io_dtype [num_pages][Hkv][page_size][D]  (16B)
+ *   block_table       int32    [batch][max_pages]: page of the tokens
+ *                     [i page_size, (i + 1) page_size) of a sequence in entry
+ *                     i.  Entries past a sequence's last token are not read.
+ * A page may appear in several sequences' rows (a shared prefix), but a call
+ * of lq_kv_append must not write one place of the cache from two tokens. */
+typedef struct {
+    void *k_pages;
+    void *v_pages;
+    const int32_t *block_table;
+    int32_t batch;      /* B in [1, 4096] (above: LQ_ERR_UNSUPPORTED)        */
+    int32_t num_pages;  /* >= 1; num_pages * Hkv < 2^31                      */
+    int32_t page_size;  /* a power of two in [16, 256] (else
+                           LQ_ERR_UNSUPPORTED)                               */
+    int32_t max_pages;  /* >= 1; max_pages * page_size < 2^30                */
+} lq_kv_cache;
+
+/* Norm and rotation of q and k in one pass, for `tokens` rows of q [tokens,
+ * Hq, D] and k [tokens, Hkv, D]: y = rotate(norm(x) * weight, position).
+ *   q, k         (16B); consecutive tokens lie q_stride / k_stride elements
+ *                apart (>= heads * D, a multiple of 16 bytes), the heads of a
+ *                token are contiguous: both may be slices of one projection's
+ *                output.  k (with k_out) may be NULL: q alone.
+ *   q_weight, k_weight  FP32 [D] (16B), or NULL for none (also for
+ *                LQ_NORM_NONE, where a weight is LQ_ERR_INVALID_ARGUMENT).
+ *   positions    int32 [tokens]; rows with a negative position are padding:
+ *                their output rows are left as they are.  NULL (only with
+ *                rot_dim == 0): every row is taken.
+ *   cos_sin      FP32 [table_len][rot_dim] (16B): row p holds the cosines and
+ *                then the sines of the rot_dim / 2 angles of position p;
+ *                NULL with rot_dim == 0.  Pair (x0, x1) becomes
+ *                (x0 cos - x1 sin, x1 cos + x0 sin).  A row with a position
+ *                >= table_len is left as it is (LQ_DEVERR_BAD_POSITION).
+ *   q_out, k_out (16B) contiguous [tokens, heads, D]; q_out may be q itself
+ *                where q_stride == Hq * D (k likewise), and must not overlap
+ *                the inputs otherwise.
+ * tokens == 0 is a no-op.  One launch. */
+LQ_API lq_status lq_qk_norm_rotate(const lq_attn_config *cfg, const void *q, int64_t q_stride,
+                                   const void *k, int64_t k_stride, const float *q_weight,
+                                   const float *k_weight, const int32_t *positions,
+                                   const float *cos_sin, int32_t table_len, int32_t tokens,
+                                   void *q_out, void *k_out, lq_stream_t stream);
+
+/* Appends new tokens' keys and values to the cache, with the norm and the
+ * rotation of lq_qk_norm_rotate applied to k on the way (v is copied), and
+ * writes the normalised and rotated q to q_out.
+ *   pos        int32 [B]: tokens of each sequence already in the cache;
+ *              negative: idle slot, whose rows are left alone.
+ *   cu_tokens  int32 [B + 1], non-decreasing from 0: rows cu_tokens[b] ..
+ *              cu_tokens[b + 1] - 1 of q, k, v are the new tokens of
+ *              sequence b; rows from cu_tokens[B] on are padding and skipped.
+ *              NULL: every sequence has tokens / B of them (tokens must be a
+ *              multiple of B).
+ *   q, k, v    [tokens, heads, D] with token strides as above; the i-th new
+ *              token of sequence b has position pos[b] + i.  q (with q_out)
+ *              may be NULL: keys and values alone.
+ * A token whose position has no row in block_table or (with rot_dim > 0) in
+ * cos_sin is skipped (LQ_DEVERR_BAD_POSITION), as is one whose page is not in
+ * [0, num_pages) (LQ_DEVERR_BAD_PAGE).  tokens == 0 is a no-op.  One launch. */
+LQ_API lq_status lq_kv_append(const lq_attn_config *cfg, const lq_kv_cache *cache,
+                              const int32_t *pos, const int32_t *cu_tokens, int32_t tokens,
+                              const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                              const void *v, int64_t v_stride, const float *q_weight,
+                              const float *k_weight, const float *cos_sin, int32_t table_len,
+                              void *q_out, lq_stream_t stream);
+
+/* Bytes of lq_attn_decode's workspace for `batch` sequences on the current
+ * device; -1 for an invalid configuration or batch. */
+LQ_API int64_t lq_attn_workspace_bytes(const lq_attn_config *cfg, int32_t batch);
+
+/* Attention of one new token per sequence over the cache, the token itself
+ * (appended before) included: for each sequence b with pos[b] >= 0 and each
+ * query head, o = softmax(cap(scale q . K^T)) V over the tokens max(0, pos[b]
+ * + 1 - window) .. pos[b].  Keys and values of other tokens are read past
+ * (they may hold anything, NaN included) and have no effect.
+ *   q  io_dtype [B, Hq, D] contiguous (16B), o the same; o rows of idle slots
+ *      are left as they are.
+ *   workspace  device memory (16B) of at least lq_attn_workspace_bytes; the
+ *      call needs nothing of its contents and leaves nothing in it for later
+ *      calls.  It must not be shared by calls whose work may overlap.
+ * A sequence with pos[b] >= max_pages * page_size is skipped
+ * (LQ_DEVERR_BAD_POSITION); a page not in [0, num_pages) is read as zeros
+ * and recorded (LQ_DEVERR_BAD_PAGE): that sequence's output is not valid.
+ * The tokens of all sequences are shared out evenly over the GPU and the
+ * parts of a sequence joined in a fixed order: results do not depend on
+ * scheduling.  Two launches. */
+LQ_API lq_status lq_attn_decode(const lq_attn_config *cfg, const lq_kv_cache *cache,
+                                const int32_t *pos, const void *q, void *o, void *workspace,
+                                size_t workspace_bytes, lq_stream_t stream);
+
+/* Attention of runs of new tokens (appended before) over the cache: the i-th
+ * new token of sequence b sees the tokens of its sequence up to and including
+ * its own position pos[b] + i (and no further back than `window`).  cu_tokens
+ * and tokens as for lq_kv_append; q, o io_dtype [tokens, Hq, D] contiguous
+ * (16B); o rows of idle slots and of padding are left as they are.  A token
+ * with a position >= max_pages * page_size leaves its row as it is
+ * (LQ_DEVERR_BAD_POSITION); bad pages as for lq_attn_decode.  tokens == 0 is
+ * a no-op.  One launch.  With io_dtype LQ_BF16 the softmax weights are
+ * rounded to BF16 for the product with V. */
+LQ_API lq_status lq_attn_prefill(const lq_attn_config *cfg, const lq_kv_cache *cache,
+                                 const int32_t *pos, const int32_t *cu_tokens, int32_t tokens,
+                                 const void *q, void *o, lq_stream_t stream);
 
 #ifdef __cplusplus
 }

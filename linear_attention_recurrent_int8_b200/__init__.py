@@ -9,7 +9,10 @@ missing or unloadable library raises.
 The functions carry the C names (``lq_state_init``, ``lq_decode_window``,
 ``lq_window_commit``, ``lq_prefill_chunk``, ``lq_state_snapshot``,
 ``lq_state_restore``, ``lq_fp32_step``, ...).  ``State`` and ``Snapshot`` own
-the torch tensors whose pointers the C structs hold.
+the torch tensors whose pointers the C structs hold.  The operators of a
+hybrid model's softmax-attention layers (``lq_qk_norm_rotate``,
+``lq_kv_append``, ``lq_attn_decode``, ``lq_attn_prefill``) are marshalled in
+``attention.py`` and offered here with the rest.
 """
 from __future__ import annotations
 
@@ -27,13 +30,17 @@ LQ_GATE_SCALAR, LQ_GATE_DIAG = 0, 1
 LQ_F32, LQ_BF16 = 0, 1
 LQ_COMP_ROWS, LQ_COMP_SVD = 0, 1
 LQ_POS_PER_SEQUENCE = -1
-LQ_DEVERR_WAIT_TIMEOUT, LQ_DEVERR_BAD_POSITION = 1, 2
+LQ_DEVERR_WAIT_TIMEOUT, LQ_DEVERR_BAD_POSITION, LQ_DEVERR_BAD_PAGE = 1, 2, 4
+LQ_NORM_NONE, LQ_NORM_L2, LQ_NORM_RMS = range(3)
+LQ_ROT_HALVES, LQ_ROT_ADJACENT = 0, 1
 
 # Every symbol include/lq.h declares.
 ABI_SYMBOLS = ("lq_buffer_elems", "lq_state_init", "lq_decode_window", "lq_decode_ragged",
                "lq_ragged_flush", "lq_window_commit",
                "lq_prefill_chunk", "lq_prefill_chunk_noalloc", "lq_prefill_workspace_bytes", "lq_state_snapshot", "lq_state_restore", "lq_fp32_step",
-               "lq_state_destroy", "lq_status_string", "lq_device_errors")
+               "lq_state_destroy", "lq_status_string", "lq_device_errors",
+               "lq_qk_norm_rotate", "lq_kv_append", "lq_attn_workspace_bytes", "lq_attn_decode",
+               "lq_attn_prefill")
 
 
 class LQError(RuntimeError):
@@ -60,6 +67,18 @@ class LqState(ctypes.Structure):
                 ("impl", ctypes.c_void_p)]
 
 
+class LqAttnConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("q_heads", "kv_heads", "head_dim", "io_dtype", "norm",
+                                              "rot_dim", "rot_pairs", "window")] + \
+        [(n, ctypes.c_float) for n in ("eps", "scale", "softcap")]
+
+
+class LqKvCache(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p)] + \
+        [(n, ctypes.c_int32) for n in ("batch", "num_pages", "page_size", "max_pages")]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -75,7 +94,8 @@ def load_library(build: bool = True):
             if not os.path.exists(LIB_PATH):
                 raise ImportError(f"liblq.so not found at {LIB_PATH}")
             lib = ctypes.CDLL(LIB_PATH)
-            P, I32 = ctypes.c_void_p, ctypes.c_int32
+            P, I32, I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+            AC, KV = ctypes.POINTER(LqAttnConfig), ctypes.POINTER(LqKvCache)
             sig = {
                 "lq_buffer_elems": (ctypes.c_int64, [ctypes.POINTER(LqConfig), I32]),
                 "lq_state_init": (I32, [ctypes.POINTER(LqState), ctypes.POINTER(LqConfig), P, P]),
@@ -94,6 +114,11 @@ def load_library(build: bool = True):
                 "lq_state_destroy": (None, [ctypes.POINTER(LqState)]),
                 "lq_status_string": (ctypes.c_char_p, [I32]),
                 "lq_device_errors": (I32, [ctypes.POINTER(ctypes.c_uint32)]),
+                "lq_qk_norm_rotate": (I32, [AC, P, I64, P, I64, P, P, P, P, I32, I32, P, P, P]),
+                "lq_kv_append": (I32, [AC, KV, P, P, I32, P, I64, P, I64, P, I64, P, P, P, I32, P, P]),
+                "lq_attn_workspace_bytes": (I64, [AC, I32]),
+                "lq_attn_decode": (I32, [AC, KV, P, P, P, P, ctypes.c_size_t, P]),
+                "lq_attn_prefill": (I32, [AC, KV, P, P, I32, P, P, P]),
             }
             for name, (res, args) in sig.items():
                 f = getattr(lib, name)
@@ -471,3 +496,7 @@ def lq_device_errors() -> int:
     flags = ctypes.c_uint32(0)
     _check(load_library().lq_device_errors(ctypes.byref(flags)), "lq_device_errors")
     return flags.value
+
+
+from .attention import (AttnConfig, KvCache, lq_attn_decode, lq_attn_prefill,  # noqa: E402,F401
+                        lq_attn_workspace_bytes, lq_kv_append, lq_qk_norm_rotate)

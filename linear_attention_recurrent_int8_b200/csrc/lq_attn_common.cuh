@@ -1,0 +1,199 @@
+// lq_attn_common.cuh -- device and host helpers shared by the attention
+// kernels over the paged cache.
+#pragma once
+
+#include <atomic>
+
+#include "lq_attn.h"
+#include "lq_common.cuh"
+#include "lq_kernels.h"
+
+namespace lq {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Box load of a 3-D map ([pages * heads][page_size][D]; no multicast).  A
+// coordinate outside the map fills zeros.
+__device__ __forceinline__ void tma_page_load(void *dst, const CUtensorMap *map, int c0, int c1, int c2,
+                                              uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// D += A B, 16 x 8 x 16, BF16 operands, FP32 sums.
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// cap tanh(s / cap), in units of log2.  For BF16 outputs by
+// tanh x = 1 - 2 / (1 + e^{2x}), whose absolute error is a few FP32 steps of
+// cap: far below a BF16 step of any output.  FP32 outputs take tanhf.
+template <bool BF16>
+__device__ __forceinline__ float capped_log2(float s, float scale, float cap) {
+    const float x = s * scale / cap;
+    if constexpr (BF16) return cap * kLog2e * (1.0f - __fdividef(2.0f, 1.0f + ex2(2.0f * kLog2e * x)));
+    else return cap * tanhf(x) * kLog2e;
+}
+
+// Programmatic dependent launch: lets the next launch of the stream start,
+// and waits for the previous one's results.
+__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A tile of query rows of one sequence: rows first .. first + rows - 1 of its
+// new tokens, in rows base + first .. of q and o; `start` tokens were in the
+// cache before.
+struct QueryTile {
+    int b, first, rows, start;
+    long long base;
+};
+
+// The tile_index-th tile of ROWS query rows over all sequences (in order);
+// rows == 0 past the last one.  All NT threads of the block take part.
+// Sequence lengths come from cu_tokens (or are all tokens / B); an idle
+// slot has no tiles, rows that would lie outside [0, tokens) or at positions
+// past the block table are cut off, the latter with the device error word set.
+template <int ROWS, int NT>
+__device__ __forceinline__ QueryTile find_query_tile(const AttnArgs &a, long long tile_index, int *smem /* NT / 32 + 6 */) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cap = a.max_pages << a.page_shift;
+    auto rows_of = [&](int b, long long &base, int &start) -> int {
+        start = __ldg(a.pos + b);
+        long long n;
+        if (a.cu) {
+            base = __ldg(a.cu + b);
+            n = __ldg(a.cu + b + 1) - base;
+        } else {
+            n = a.tokens / a.B;
+            base = b * n;
+        }
+        if (start < 0 || base < 0) return 0;
+        if (n > a.tokens - base) n = a.tokens - base;
+        if (n > (long long)cap - start) {
+            if (tile_index == 0 && blockIdx.y == 0 && n > 0) atomicOr(&g_dev_error, kErrBadPosition);
+            n = (long long)cap - start;
+        }
+        return n > 0 ? (int)n : 0;
+    };
+    const int chunk = (a.B + NT - 1) / NT;
+    long long base;
+    int start, mine = 0;
+    for (int i = 0; i < chunk; ++i) {
+        const int b = tid * chunk + i;
+        if (b < a.B) mine += (rows_of(b, base, start) + ROWS - 1) / ROWS;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += y;
+    }
+    if (lane == 31) smem[warp] = incl;
+    int *found = smem + NT / 32;
+    if (tid == 0) found[2] = 0;
+    __syncthreads();
+    long long at = incl - mine;
+    for (int w = 0; w < warp; ++w) at += smem[w];
+    if (tile_index >= at && tile_index < at + mine) {
+        for (int i = 0; i < chunk; ++i) {
+            const int b = tid * chunk + i;
+            if (b >= a.B) break;
+            const int n = rows_of(b, base, start), t = (n + ROWS - 1) / ROWS;
+            if (tile_index < at + t) {
+                const int first = (int)(tile_index - at) * ROWS;
+                found[0] = b;
+                found[1] = first;
+                found[2] = min(ROWS, n - first);
+                found[3] = start;
+                found[4] = (int)base;
+                break;
+            }
+            at += t;
+        }
+    }
+    __syncthreads();
+    QueryTile q;
+    q.b = found[0], q.first = found[1], q.rows = found[2], q.start = found[3], q.base = found[4];
+    return q;
+}
+
+// Tiles of ROWS query rows that `tokens` rows of B sequences can have.
+inline long long query_tiles(const AttnArgs &a, int rows) {
+    if (!a.cu) return (long long)a.B * ((a.tokens / a.B + rows - 1) / rows);
+    return (long long)a.tokens / rows + (a.B < a.tokens ? a.B : a.tokens);
+}
+
+// Map of the cache pages as [num_pages * Hkv][page_size][D], boxes of 128
+// bytes x `rows` tokens stored with the 128-byte swizzle.
+inline bool page_map(CUtensorMap *m, const void *base, int D, const AttnArgs &a, bool bf16, int rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t es = bf16 ? 2 : 4;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.page_size, (cuuint64_t)a.num_pages * a.Hkv};
+    const cuuint64_t strides[2] = {D * es, D * es * a.page_size};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)rows, 1};
+    const cuuint32_t one[3] = {1, 1, 1};
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+               const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// SM count of the current device, looked up once per device.
+inline cudaError_t device_sms(int *sms) {
+    static std::atomic<int> count[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int n = count[dev & 63].load(std::memory_order_relaxed);
+    if (n == 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        count[dev & 63].store(n, std::memory_order_relaxed);
+    }
+    *sms = n;
+    return cudaSuccess;
+}
+
+// Raises a kernel's shared-memory limit once per device.
+template <typename K>
+cudaError_t allow_smem(K kern, std::atomic<uint64_t> &done, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
+
+}  // namespace lq
