@@ -76,13 +76,14 @@ struct QueryTile {
     long long base;
 };
 
-// The tile_index-th tile of ROWS query rows over all sequences (in order);
+// The tile_index-th tile of `rows` query rows over all sequences (in order);
 // rows == 0 past the last one.  All NT threads of the block take part.
 // Sequence lengths come from cu_tokens (or are all tokens / B); an idle
 // slot has no tiles, rows that would lie outside [0, tokens) or at positions
 // past the block table are cut off, the latter with the device error word set.
-template <int ROWS, int NT>
-__device__ __forceinline__ QueryTile find_query_tile(const AttnArgs &a, long long tile_index, int *smem /* NT / 32 + 6 */) {
+template <int NT>
+__device__ __forceinline__ QueryTile find_query_tile(const AttnArgs &a, int rows, long long tile_index,
+                                                     int *smem /* NT / 32 + 6 */) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cap = a.max_pages << a.page_shift;
     auto rows_of = [&](int b, long long &base, int &start) -> int {
@@ -108,7 +109,7 @@ __device__ __forceinline__ QueryTile find_query_tile(const AttnArgs &a, long lon
     int start, mine = 0;
     for (int i = 0; i < chunk; ++i) {
         const int b = tid * chunk + i;
-        if (b < a.B) mine += (rows_of(b, base, start) + ROWS - 1) / ROWS;
+        if (b < a.B) mine += (rows_of(b, base, start) + rows - 1) / rows;
     }
     int incl = mine;
 #pragma unroll
@@ -126,12 +127,12 @@ __device__ __forceinline__ QueryTile find_query_tile(const AttnArgs &a, long lon
         for (int i = 0; i < chunk; ++i) {
             const int b = tid * chunk + i;
             if (b >= a.B) break;
-            const int n = rows_of(b, base, start), t = (n + ROWS - 1) / ROWS;
+            const int n = rows_of(b, base, start), t = (n + rows - 1) / rows;
             if (tile_index < at + t) {
-                const int first = (int)(tile_index - at) * ROWS;
+                const int first = (int)(tile_index - at) * rows;
                 found[0] = b;
                 found[1] = first;
-                found[2] = min(ROWS, n - first);
+                found[2] = min(rows, n - first);
                 found[3] = start;
                 found[4] = (int)base;
                 break;
@@ -145,7 +146,7 @@ __device__ __forceinline__ QueryTile find_query_tile(const AttnArgs &a, long lon
     return q;
 }
 
-// Tiles of ROWS query rows that `tokens` rows of B sequences can have.
+// Tiles of `rows` query rows that `tokens` rows of B sequences can have.
 inline long long query_tiles(const AttnArgs &a, int rows) {
     if (!a.cu) return (long long)a.B * ((a.tokens / a.B + rows - 1) / rows);
     return (long long)a.tokens / rows + (a.B < a.tokens ? a.B : a.tokens);

@@ -5,6 +5,7 @@
 // shared memory as FP32, 4 x 4 register tiles of FP32 FMAs, running maximum
 // and sum per row.
 #include "lq_attn_common.cuh"
+#include "lq_tc.cuh"
 
 namespace lq {
 namespace {
@@ -18,19 +19,11 @@ struct Simt {
     static constexpr int kSmem = (kRows * kLd + kKeys * kLd + kKeys * D + kRows * (kKeys + 4)) * 4;
 };
 
-// Four consecutive io elements.
-template <bool BF16>
 __device__ __forceinline__ float4 load4(const void *p, size_t i) {
-    if constexpr (BF16) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p) + i);
-        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                           __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
-    } else {
-        return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-    }
+    return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
 }
 
-template <int D, bool BF16>
+template <int D>
 __global__ void __launch_bounds__(256) attn_prefill_simt(const AttnArgs a) {
     using S = Simt<D>;
     constexpr int LD = S::kLd, KT = S::kKeys, NC = S::kCols, PL = KT + 4;
@@ -38,14 +31,14 @@ __global__ void __launch_bounds__(256) attn_prefill_simt(const AttnArgs a) {
     float *qs = sm, *ks = qs + S::kRows * LD, *vs = ks + KT * LD, *ps = vs + KT * D;
     __shared__ int find[S::kThreads / 32 + 6];
     // the last tiles see the most keys: they go first
-    const QueryTile qt = find_query_tile<S::kRows, S::kThreads>(a, gridDim.x - 1 - (long long)blockIdx.x, find);
+    const QueryTile qt = find_query_tile<S::kThreads>(a, S::kRows, gridDim.x - 1 - (long long)blockIdx.x, find);
     if (qt.rows <= 0) return;
     const int tid = threadIdx.x, rg = tid >> 4, cg = tid & 15;
     const int h = blockIdx.y, kv = h / (a.Hq / a.Hkv);
     for (int i = tid; i < S::kRows * (D / 4); i += S::kThreads) {
         const int r = i / (D / 4), c = 4 * (i % (D / 4));
         float4 x = make_float4(0, 0, 0, 0);
-        if (r < qt.rows) x = load4<BF16>(a.q, ((size_t)(qt.base + qt.first + r) * a.Hq + h) * D + c);
+        if (r < qt.rows) x = load4(a.q, ((size_t)(qt.base + qt.first + r) * a.Hq + h) * D + c);
         *reinterpret_cast<float4 *>(qs + r * LD + c) = x;
     }
     const int p0 = qt.start + qt.first;               // position of row 0
@@ -67,8 +60,8 @@ __global__ void __launch_bounds__(256) attn_prefill_simt(const AttnArgs a) {
                 const int page = __ldg(a.block_table + (size_t)qt.b * a.max_pages + (tok >> a.page_shift));
                 if (page >= 0 && page < a.num_pages) {
                     const size_t at = (((size_t)page * a.Hkv + kv) * a.page_size + (tok & (a.page_size - 1))) * D + c;
-                    kx = load4<BF16>(a.k_pages, at);
-                    vx = load4<BF16>(a.v_pages, at);
+                    kx = load4(a.k_pages, at);
+                    vx = load4(a.v_pages, at);
                 } else if (c == 0) {
                     atomicOr(&g_dev_error, kErrBadPage);
                 }
@@ -107,7 +100,7 @@ __global__ void __launch_bounds__(256) attn_prefill_simt(const AttnArgs a) {
             for (int j = 0; j < NC; ++j) {
                 const int tok = k0 + cg + 16 * j;
                 const bool seen = tok <= p && (a.window == 0 || tok > p - a.window);
-                float x = a.softcap > 0.0f ? capped_log2<BF16>(s[r][j], a.scale, a.softcap) : s[r][j] * (a.scale * kLog2e);
+                float x = a.softcap > 0.0f ? capped_log2<false>(s[r][j], a.scale, a.softcap) : s[r][j] * (a.scale * kLog2e);
                 s[r][j] = seen ? x : -INFINITY;
                 mx = fmaxf(mx, s[r][j]);
             }
@@ -157,15 +150,15 @@ __global__ void __launch_bounds__(256) attn_prefill_simt(const AttnArgs a) {
         for (int e = 0; e < D / 64; ++e)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                store_io<BF16>(a.o, ((size_t)(qt.base + qt.first + row) * a.Hq + h) * D + 64 * e + 4 * cg + i, o[r][4 * e + i] * f);
+                store_io<false>(a.o, ((size_t)(qt.base + qt.first + row) * a.Hq + h) * D + 64 * e + 4 * cg + i, o[r][4 * e + i] * f);
     }
 }
 
-template <int D, bool BF16>
+template <int D>
 cudaError_t launch_simt(const AttnArgs &a, cudaStream_t stream) {
     using S = Simt<D>;
     static std::atomic<uint64_t> ready{0};
-    auto kern = attn_prefill_simt<D, BF16>;
+    auto kern = attn_prefill_simt<D>;
     const cudaError_t e = allow_smem(kern, ready, S::kSmem);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)query_tiles(a, S::kRows), (unsigned)a.Hq);
@@ -173,13 +166,394 @@ cudaError_t launch_simt(const AttnArgs &a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// BF16: tensor cores
+// ---------------------------------------------------------------------------
+
+// 128 consecutive TMEM columns of the warp's 32 lanes; the wait is part of the statement.
+__device__ __forceinline__ void tmem_load_row(uint32_t taddr, float (&v)[128]) {
+    uint32_t r[128];
+    asm volatile(
+        "{ tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n\t"
+        "tcgen05.wait::ld.sync.aligned; }"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]), "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]), "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_load_row(uint32_t taddr, float (&v)[64]) { tmem_load64(taddr, v); }
+
+// D (TMEM) = A (TMEM) B (+ D when `accumulate`), BF16, issued by one thread.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            bool accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+// Shared-memory descriptor of an MN-major operand stored with the 128-byte
+// swizzle: blocks of 64 MN elements (128 bytes) by K rows, 8 K rows to an
+// atom of 1024 bytes (the stride byte offset), `block` bytes from one block
+// of 64 MN elements to the next (the leading byte offset).
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t block) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((block >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+template <int D>
+struct Tc {
+    static constexpr int kStreams = D == 256 ? 1 : 2;     // query tiles of 128 rows
+    static constexpr int kKeys = D == 256 ? 64 : 128;     // keys of a tile
+    static constexpr int kHalves = D / 64;                // 128-byte column blocks
+    static constexpr int kQBytes = 128 * D * 2;           // a query tile
+    static constexpr int kSlotBytes = kKeys * D * 2;      // a tile of K or V
+    static constexpr int kSlots = (kStreams * kQBytes + 5 * kSlotBytes) <= 225 * 1024 ? 5 : 4;
+    static constexpr int kSoftWarps = 4 * kStreams;
+    static constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
+    static constexpr int kThreads = (kSoftWarps + 2) * 32;
+    static constexpr int kSmem = 1024 + kStreams * kQBytes + kSlots * kSlotBytes;
+    // TMEM columns: scores (two tiles: one per stream, or two of one stream),
+    // whose first half the weights overwrite, then the outputs
+    static constexpr uint32_t kColS = 0, kColO = 256;
+};
+
+struct TcBars {
+    uint64_t q_full, kv_full[5], kv_empty[5], s_full[2], p_ready[2], o_done[2], tail;
+};
+
+// One block: 128 kStreams rows, each a (token, head) pair of `group` heads
+// that share a key-value head (head fastest), against the tiles of keys.
+template <int D, bool CAP>
+__global__ void __launch_bounds__(Tc<D>::kThreads, 1)
+    attn_prefill_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                    const __grid_constant__ CUtensorMap vmap, const AttnArgs a, const int group_shift, const int box_shift) {
+    using T = Tc<D>;
+    constexpr int NS = T::kStreams, KT = T::kKeys, NH = T::kHalves;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *qs = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    unsigned char *ring = qs + NS * T::kQBytes;
+    __shared__ TcBars bars;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int find[T::kThreads / 32 + 6];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tokens = 128 * NS >> group_shift;  // of a block
+    // the last tiles see the most keys: they go first
+    const QueryTile qt = find_query_tile<T::kThreads>(a, tokens, gridDim.x - 1 - (long long)blockIdx.x, find);
+    if (qt.rows <= 0) return;
+    const int h0 = blockIdx.y << group_shift, kv = h0 / (a.Hq / a.Hkv);
+    const int p0 = qt.start + qt.first, len = p0 + qt.rows;  // keys any row sees: lo .. len - 1
+    const int lo = a.window > 0 && p0 + 1 > a.window ? p0 + 1 - a.window : 0;
+    const int k_first = lo / KT, n = (len - 1) / KT - k_first + 1;
+
+    if (tid == 0) {
+        mbar_init(&bars.q_full, 1);
+        for (int i = 0; i < T::kSlots; ++i) mbar_init(&bars.kv_full[i], 1), mbar_init(&bars.kv_empty[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&bars.s_full[i], 1), mbar_init(&bars.p_ready[i], 4), mbar_init(&bars.o_done[i], 1);
+        mbar_init(&bars.tail, 1);
+    }
+    if (warp == T::kMmaWarp) tmem_alloc(&tmem_slot, 512);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tm = tmem_slot;
+
+    if (warp == T::kLoadWarp) {
+        // ------------------------------------------------------------ TMA
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&bars.q_full, NS * T::kQBytes);
+            const int t0 = (int)(qt.base + qt.first), per = 128 >> group_shift;
+            for (int s = 0; s < NS; ++s)
+                for (int x = 0; x < NH; ++x)
+                    tma_page_load(qs + s * T::kQBytes + x * 16384, &qmap, 64 * x, h0, t0 + s * per, &bars.q_full);
+        }
+        const int box_rows = 1 << box_shift, boxes = KT >> box_shift;
+        int slot = 0, use = 0, tail_phase = 0;
+        bool ok = true;
+        // tile j of K or V into the next slot
+        auto load = [&](const CUtensorMap *map, int j, bool is_v) {
+            if (use > 0 && !mbar_wait_bounded(&bars.kv_empty[slot], (use - 1) & 1)) return false;
+            unsigned char *dst = ring + slot * T::kSlotBytes;
+            const int k0 = (k_first + j) * KT;
+            // V rows that no query row sees may hold NaN, which a weight of
+            // zero does not silence: such a tile is cleared there first
+            const bool clear = is_v && (k0 < lo || k0 + KT > len);
+            uint64_t *bar = clear ? &bars.tail : &bars.kv_full[slot];
+            if (lane == 0) mbar_arrive_expect_tx(bar, T::kSlotBytes);
+            __syncwarp();
+            for (int i = lane; i < boxes * NH; i += 32) {
+                const int bx = i / NH, x = i - bx * NH, tok = k0 + bx * box_rows;
+                int z = -1, row = 0;  // boxes past the visible keys are filled with zeros
+                if (tok < len && tok + box_rows > lo) {
+                    const int page = __ldg(a.block_table + (size_t)qt.b * a.max_pages + (tok >> a.page_shift));
+                    if (page >= 0 && page < a.num_pages) z = page * a.Hkv + kv, row = tok & (a.page_size - 1);
+                    else atomicOr(&g_dev_error, kErrBadPage);
+                }
+                tma_page_load(dst + x * (KT * 128) + bx * box_rows * 128, map, 64 * x, row, z, bar);
+            }
+            if (clear) {
+                if (!mbar_wait_bounded(&bars.tail, tail_phase)) return false;
+                tail_phase ^= 1;
+                for (int i = lane; i < KT * D / 8; i += 32) {
+                    const int r = i / (D / 8), c = i - r * (D / 8);
+                    if (k0 + r >= lo && k0 + r < len) continue;
+                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * (KT * 128) + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.kv_full[slot]);
+            }
+            if (++slot == T::kSlots) slot = 0, ++use;
+            return true;
+        };
+        // in the order the MMA lane takes them
+        ok = load(&kmap, 0, false);
+        for (int j = 0; ok && j < n; ++j) {
+            if (NS == 1 && j + 1 < n) ok = load(&kmap, j + 1, false);
+            if (ok) ok = load(&vmap, j, true);
+            if (NS == 2 && ok && j + 1 < n) ok = load(&kmap, j + 1, false);
+        }
+    } else if (warp == T::kMmaWarp) {
+        // ------------------------------------------------------------ MMAs
+        if (lane == 0) {
+            constexpr uint32_t id_qk = idesc_bf16(128, KT, false, false), id_pv = idesc_bf16(128, D, false, true);
+            int slot = 0, use = 0;
+            auto take = [&](int &at) {
+                at = slot;
+                const bool ok = mbar_wait_bounded(&bars.kv_full[slot], use & 1);
+                if (++slot == T::kSlots) slot = 0, ++use;
+                return ok;
+            };
+            auto qk = [&](int s, int at, uint32_t col) {  // scores of stream s at TMEM column col
+                const uint32_t qa = smem_u32(qs + s * T::kQBytes), ka = smem_u32(ring + at * T::kSlotBytes);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k & 3) * 32;
+                    mma_bf16(tm + col, smem_desc_sw128(qa + (k >> 2) * 16384 + off),
+                             smem_desc_sw128(ka + (k >> 2) * (KT * 128) + off), id_qk, k > 0);
+                }
+            };
+            auto pv = [&](int s, int at, uint32_t col, bool add) {
+                const uint32_t va = smem_u32(ring + at * T::kSlotBytes);
+#pragma unroll
+                for (int k = 0; k < KT / 16; ++k)
+                    mma_bf16_ta(tm + T::kColO + s * D, tm + col + 8 * k, smem_desc_mn_sw128(va + k * 2048, KT * 128), id_pv,
+                                add || k > 0);
+            };
+            bool ok = mbar_wait_bounded(&bars.q_full, 0);
+            int ks = 0, vs = 0;
+            ok = ok && take(ks);
+            if (ok) {
+                tc_fence_after_sync();
+#pragma unroll
+                for (int s = 0; s < NS; ++s) {
+                    qk(s, ks, T::kColS + s * KT);
+                    mma_commit(&bars.s_full[s]);
+                }
+                mma_commit(&bars.kv_empty[ks]);
+            }
+            for (int j = 0; ok && j < n; ++j) {
+                const bool more = j + 1 < n;
+                if constexpr (NS == 2) {
+                    ok = take(vs) && (!more || take(ks));
+                    for (int s = 0; ok && s < 2; ++s) {
+                        ok = mbar_wait_bounded(&bars.p_ready[s], j & 1);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        pv(s, vs, T::kColS + s * KT, j > 0);
+                        if (more) {
+                            qk(s, ks, T::kColS + s * KT);
+                            mma_commit(&bars.s_full[s]);
+                        } else {
+                            mma_commit(&bars.o_done[s]);
+                        }
+                    }
+                    if (ok) {
+                        mma_commit(&bars.kv_empty[vs]);
+                        if (more) mma_commit(&bars.kv_empty[ks]);
+                    }
+                } else {
+                    if (more) {
+                        ok = take(ks);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        qk(0, ks, T::kColS + ((j + 1) & 1) * KT);
+                        mma_commit(&bars.s_full[(j + 1) & 1]);
+                        mma_commit(&bars.kv_empty[ks]);
+                    }
+                    ok = take(vs) && mbar_wait_bounded(&bars.p_ready[0], j & 1);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    pv(0, vs, T::kColS + (j & 1) * KT, j > 0);
+                    mma_commit(&bars.o_done[0]);
+                    mma_commit(&bars.kv_empty[vs]);
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax: one row per thread
+        const int s = warp >> 2, q4 = warp & 3;
+        const int R = s * 128 + 32 * q4 + lane;
+        const int tok = R >> group_shift, head = h0 + (R & ((1 << group_shift) - 1));
+        const int p = p0 + tok;
+        // positions of the warp's rows
+        const int pw0 = p0 + ((s * 128 + 32 * q4) >> group_shift), pw1 = p0 + ((s * 128 + 32 * q4 + 31) >> group_shift);
+        const uint32_t lanes = tm + ((uint32_t)(32 * q4) << 16);
+        const uint32_t oa = lanes + T::kColO + s * D;
+        // scores enter as 2^(c x): c = log2(e) |scale| (never 0, so that a
+        // masked score stays -inf), or 1 for capped scores
+        const float c = CAP ? 1.0f : fmaxf(fabsf(a.scale * kLog2e), 1e-30f);
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            const int buf = NS == 2 ? s : (j & 1);
+            const uint32_t sa = lanes + T::kColS + buf * KT;
+            if (!mbar_wait_bounded(&bars.s_full[buf], NS == 2 ? (j & 1) : ((j >> 1) & 1))) { ok = false; break; }
+            tc_fence_after_sync();
+            float x[KT];
+            tmem_load_row(sa, x);
+            if constexpr (CAP) {
+#pragma unroll
+                for (int i = 0; i < KT; ++i) x[i] = capped_log2<true>(x[i], a.scale, a.softcap);
+            } else if (a.scale < 0.0f) {
+#pragma unroll
+                for (int i = 0; i < KT; ++i) x[i] = -x[i];
+            }
+            const int k0 = (k_first + j) * KT;
+            if (k0 + KT - 1 > pw0 || (a.window > 0 && k0 <= pw1 - a.window)) {
+                const int hi = p - k0, first = a.window > 0 ? hi - a.window + 1 : 0;
+#pragma unroll
+                for (int i = 0; i < KT; ++i)
+                    if (i > hi || i < first) x[i] = -INFINITY;
+            }
+            float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int i = 4; i < KT; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+            const float tile_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // the reference maximum moves only when the weights would pass
+            // 2^8: the output tile in TMEM is rescaled in few of the steps
+            if (NS == 1 && j > 0) {
+                // two score tiles: these scores say nothing about the last
+                // product with V, whose output may be rescaled now and whose
+                // weights' barrier must have been passed
+                if (!mbar_wait_bounded(&bars.o_done[0], (j - 1) & 1)) { ok = false; break; }
+                tc_fence_after_sync();
+            }
+            const bool grow = tile_max > m && (m == -INFINITY || (tile_max - m) * c > 8.0f);
+            if (__any_sync(0xffffffffu, grow)) {
+                const float f = grow ? ex2((m - tile_max) * c) : 1.0f;  // m = -inf: 0
+                if (grow) m = tile_max, l *= f;
+                if (j > 0) {
+#pragma unroll 1
+                    for (int k = 0; k < D; k += 32) {
+                        float o[32];
+                        tmem_load32(oa + k, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] *= f;
+                        tmem_store32(oa + k, o);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.0f : m * c;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < KT; k += 64) {
+                float w[32];
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    const float e0 = ex2(fmaf(x[k + i], c, -base)), e1 = ex2(fmaf(x[k + i + 1], c, -base));
+                    sum[i & 2] += e0, sum[(i & 2) + 1] += e1;
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
+                    w[i / 2] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&h));
+                }
+                tmem_store32(sa + k / 2, w);
+            }
+            l += (sum[0] + sum[2]) + (sum[1] + sum[3]);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.p_ready[s]);
+        }
+        if (ok && mbar_wait_bounded(&bars.o_done[s], NS == 2 ? 0 : (n - 1) & 1)) {
+            tc_fence_after_sync();
+            const float f = 1.0f / l;
+            __nv_bfloat16 *op = static_cast<__nv_bfloat16 *>(a.o) + ((size_t)(qt.base + qt.first + tok) * a.Hq + head) * D;
+#pragma unroll 1
+            for (int k = 0; k < D; k += 32) {
+                float o[32];
+                tmem_load32(oa + k, o);
+                if (tok < qt.rows) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(o[i + 2 * e] * f, o[i + 2 * e + 1] * f);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                        *reinterpret_cast<uint4 *>(op + k + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == T::kMmaWarp) {
+        tc_fence_after_sync();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+// Map of q [tokens, Hq, D]: boxes of 64 channels x `heads` heads x 128 / heads tokens.
+bool query_map(CUtensorMap *m, const AttnArgs &a, int D, int heads) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.Hq * D * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)(128 / heads)};
+    const cuuint32_t one[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool CAP>
+cudaError_t launch_tc(const AttnArgs &a, cudaStream_t stream) {
+    using T = Tc<D>;
+    static std::atomic<uint64_t> ready{0};
+    auto kern = attn_prefill_tc<D, CAP>;
+    const cudaError_t e = allow_smem(kern, ready, T::kSmem);
+    if (e != cudaSuccess) return e;
+    // heads of a block: the power of two in Hq / Hkv, at most 32
+    const int G = a.Hq / a.Hkv;
+    int gs = 0, bs = a.page_shift;
+    while (gs < 5 && (G >> gs) % 2 == 0) ++gs;
+    while ((1 << bs) > T::kKeys) --bs;
+    CUtensorMap qm, km, vm;
+    if (!query_map(&qm, a, D, 1 << gs) || !page_map(&km, a.k_pages, D, a, true, 1 << bs) ||
+        !page_map(&vm, a.v_pages, D, a, true, 1 << bs))
+        return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)query_tiles(a, 128 * T::kStreams >> gs), (unsigned)(a.Hq >> gs));
+    kern<<<grid, T::kThreads, T::kSmem, stream>>>(qm, km, vm, a, gs, bs);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_tc_d(const AttnArgs &a, cudaStream_t stream) {
+    return a.softcap > 0.0f ? launch_tc<D, true>(a, stream) : launch_tc<D, false>(a, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_attn_prefill(const AttnArgs &a, int D, bool bf16, cudaStream_t stream) {
     switch (D) {
-        case 64: return bf16 ? launch_simt<64, true>(a, stream) : launch_simt<64, false>(a, stream);
-        case 128: return bf16 ? launch_simt<128, true>(a, stream) : launch_simt<128, false>(a, stream);
-        case 256: return bf16 ? launch_simt<256, true>(a, stream) : launch_simt<256, false>(a, stream);
+        case 64: return bf16 ? launch_tc_d<64>(a, stream) : launch_simt<64>(a, stream);
+        case 128: return bf16 ? launch_tc_d<128>(a, stream) : launch_simt<128>(a, stream);
+        case 256: return bf16 ? launch_tc_d<256>(a, stream) : launch_simt<256>(a, stream);
     }
     return cudaErrorInvalidValue;
 }
