@@ -498,5 +498,19 @@ def lq_device_errors() -> int:
     return flags.value
 
 
-from .attention import (AttnConfig, KvCache, lq_attn_decode, lq_attn_prefill,  # noqa: E402,F401
-                        lq_attn_workspace_bytes, lq_kv_append, lq_qk_norm_rotate)
+# --------------------------------------------------------------------------
+# The softmax-attention operators (attention.py, which imports torch: loaded
+# on first use, as nothing else here needs torch at import time)
+# --------------------------------------------------------------------------
+
+_ATTENTION = ("AttnConfig", "KvCache", "lq_qk_norm_rotate", "lq_kv_append", "lq_attn_workspace_bytes",
+              "lq_attn_decode", "lq_attn_prefill")
+
+
+def __getattr__(name: str):
+    if name in _ATTENTION:
+        from . import attention
+        for n in _ATTENTION:
+            globals()[n] = getattr(attention, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -8,11 +8,16 @@ current stream of the tensors' device is used.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from dataclasses import dataclass
 
+import torch
+
 import linear_attention_recurrent_int8_b200 as _lq
+
+_Tensor, _f32, _i32 = torch.Tensor, torch.float32, torch.int32
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 @dataclass(frozen=True)
@@ -37,15 +42,13 @@ class AttnConfig:
                              self.softcap)
         object.__setattr__(self, "_c", c)
         object.__setattr__(self, "_ref", ctypes.byref(c))
+        object.__setattr__(self, "_layout", (self.kv_heads, self.head_dim, self.io_dtype))
+        object.__setattr__(self, "io_torch_dtype",
+                           torch.bfloat16 if self.io_dtype == _lq.LQ_BF16 else torch.float32)
 
     def c(self):
         """The C struct (its values are those given at construction)."""
         return self._c
-
-    @property
-    def io_torch_dtype(self):
-        import torch
-        return torch.bfloat16 if self.io_dtype == _lq.LQ_BF16 else torch.float32
 
 
 class KvCache:
@@ -55,7 +58,6 @@ class KvCache:
     contents may change between calls; the tensors are fixed."""
 
     def __init__(self, cfg: AttnConfig, k_pages, v_pages, block_table):
-        import torch
         for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
             _check_dense(t, name, cfg.io_torch_dtype)
             if t.dim() != 4 or t.shape[1] != cfg.kv_heads or t.shape[3] != cfg.head_dim:
@@ -69,7 +71,7 @@ class KvCache:
         if v_pages.device != k_pages.device or block_table.device != k_pages.device:
             raise ValueError("k_pages, v_pages and block_table: on different devices")
         self._tensors = (k_pages, v_pages, block_table)
-        self.layout = (cfg.kv_heads, cfg.head_dim, cfg.io_dtype)
+        self.layout = cfg._layout
         self.device = k_pages.device
         self.batch, self.max_pages = block_table.shape
         self.num_pages, _, self.page_size, _ = k_pages.shape
@@ -96,12 +98,15 @@ class KvCache:
 # --------------------------------------------------------------------------
 # Argument checks
 # --------------------------------------------------------------------------
+#
+# These run on every call of a decode step, whose kernels take a few
+# microseconds: each check asks a tensor for as little as it needs, and the
+# devices are compared by index.
 
 def _check_dense(t, name: str, dtype):
-    import torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
@@ -116,10 +121,9 @@ def _check_vector(t, name: str, dtype, numel: int):
 def _rows(t, name: str, cfg: AttnConfig, heads: int):
     """(tokens, token stride) of a [..., heads, head_dim] tensor whose heads
     are contiguous and whose tokens lie at one stride."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != cfg.io_torch_dtype:
+    if t.dtype is not cfg.io_torch_dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {cfg.io_torch_dtype}")
     shape = t.shape
     d = cfg.head_dim
@@ -130,6 +134,8 @@ def _rows(t, name: str, cfg: AttnConfig, heads: int):
     strides = t.stride()
     if strides[-1] != 1 or (heads > 1 and strides[-2] != d):
         raise ValueError(f"{name}: the heads of a token are not contiguous (strides {strides})")
+    if len(shape) == 3 and shape[0] > 1:
+        return shape[0], strides[0]
     tokens, stride = 1, None  # leading dimensions, innermost first, as one
     for n, s in zip(reversed(shape[:-2]), reversed(strides[:-2])):
         if n == 1:
@@ -144,64 +150,78 @@ def _rows(t, name: str, cfg: AttnConfig, heads: int):
 
 def _check_out(t, name: str, cfg: AttnConfig, tokens: int, heads: int):
     _check_dense(t, name, cfg.io_torch_dtype)
-    if t.numel() != tokens * heads * cfg.head_dim or t.shape[-2:] != (heads, cfg.head_dim):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tokens} rows of [{heads}, {cfg.head_dim}]")
+    shape = t.shape
+    if t.numel() != tokens * heads * cfg.head_dim or len(shape) < 2 or shape[-1] != cfg.head_dim or \
+            shape[-2] != heads:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected {tokens} rows of [{heads}, {cfg.head_dim}]")
 
 
 def _check_weights(cfg: AttnConfig, q_weight, k_weight):
-    import torch
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _check_vector(w, name, torch.float32, cfg.head_dim)
+    if q_weight is not None:
+        _check_vector(q_weight, "q_weight", _f32, cfg.head_dim)
+    if k_weight is not None:
+        _check_vector(k_weight, "k_weight", _f32, cfg.head_dim)
 
 
 def _table_len(cfg: AttnConfig, cos_sin) -> int:
-    import torch
     if cos_sin is None:
         return 0
-    _check_dense(cos_sin, "cos_sin", torch.float32)
-    if cos_sin.dim() != 2 or cos_sin.shape[1] != cfg.rot_dim:
-        raise ValueError(f"cos_sin: shape {tuple(cos_sin.shape)}, expected [positions, {cfg.rot_dim}]")
-    return cos_sin.shape[0]
+    _check_dense(cos_sin, "cos_sin", _f32)
+    shape = cos_sin.shape
+    if len(shape) != 2 or shape[1] != cfg.rot_dim:
+        raise ValueError(f"cos_sin: shape {tuple(shape)}, expected [positions, {cfg.rot_dim}]")
+    return shape[0]
 
 
-def _check_devices(device, *named):
-    for t, name in named:
-        if t is not None and (t.device.type != "cuda" or t.device != device):
-            raise ValueError(f"{name}: on {t.device}, expected a CUDA tensor on {device}"
-                             if device.type == "cuda" else f"{name}: on {t.device}, expected a CUDA tensor")
+def _check_devices(*tensors) -> int:
+    """Index of the CUDA device that all of the tensors (None aside) are on."""
+    first = None
+    for t in tensors:
+        if t is not None:
+            i = t.get_device()  # -1 on the host
+            if i < 0:
+                raise ValueError(f"expected CUDA tensors, one {tuple(t.shape)} is on {t.device}")
+            if first is None:
+                first = i
+            elif i != first:
+                raise ValueError(f"a tensor {tuple(t.shape)} is on {t.device}, others are on cuda:{first}")
+    return first
 
 
 def _check_cache(cfg: AttnConfig, cache: KvCache):
     if not isinstance(cache, KvCache):
         raise TypeError(f"cache: expected a KvCache, got {type(cache).__name__}")
-    if cache.layout != (cfg.kv_heads, cfg.head_dim, cfg.io_dtype):
-        raise ValueError(f"cache: made for (kv_heads, head_dim, io_dtype) {cache.layout}, not "
-                         f"{(cfg.kv_heads, cfg.head_dim, cfg.io_dtype)}")
+    if cache.layout != cfg._layout:
+        raise ValueError(f"cache: made for (kv_heads, head_dim, io_dtype) {cache.layout}, not {cfg._layout}")
 
 
 def _check_places(cache: KvCache, pos, cu_tokens, tokens: int):
-    import torch
-    _check_vector(pos, "pos", torch.int32, cache.batch)
+    _check_vector(pos, "pos", _i32, cache.batch)
     if cu_tokens is not None:
-        _check_vector(cu_tokens, "cu_tokens", torch.int32, cache.batch + 1)
+        _check_vector(cu_tokens, "cu_tokens", _i32, cache.batch + 1)
     elif tokens % cache.batch != 0:
         raise ValueError(f"{tokens} tokens for {cache.batch} sequences need cu_tokens")
 
 
-_no_switch = contextlib.nullcontext()
-
-
-def _on(device, stream):
-    """(context that makes `device` current, cudaStream_t) of a call."""
-    import torch
+def _stream_on(index: int, stream) -> int:
+    """cudaStream_t of a call on device `index`."""
     if stream is None:
-        raw = torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream: on {stream.device}, expected cuda:{index}")
+    return stream.cuda_stream
+
+
+def _call(index: int, name: str, *args):
+    """The C function with device `index` current."""
+    f = getattr(_lq.load_library(), name)
+    if _current_device() == index:
+        status = f(*args)
     else:
-        if stream.device != device:
-            raise ValueError(f"stream: on {stream.device}, expected {device}")
-        raw = stream.cuda_stream
-    return (_no_switch if torch.cuda.current_device() == device.index else torch.cuda.device(device)), raw
+        with torch.cuda.device(index):
+            status = f(*args)
+    if status != _lq.LQ_OK:
+        _lq._check(status, name)
 
 
 def _p(t):
@@ -217,7 +237,6 @@ def lq_qk_norm_rotate(cfg: AttnConfig, q, k, q_weight, k_weight, positions, cos_
     """Norm and rotation of q [..., tokens, q_heads, head_dim] and k [...,
     tokens, kv_heads, head_dim] (k and k_out may be None) into q_out and
     k_out; q and k may be token-strided slices of one projection's output."""
-    import torch
     n, q_stride = _rows(q, "q", cfg, cfg.q_heads)
     k_stride = 0
     _check_out(q_out, "q_out", cfg, n, cfg.q_heads)
@@ -231,15 +250,11 @@ def lq_qk_norm_rotate(cfg: AttnConfig, q, k, q_weight, k_weight, positions, cos_
     _check_weights(cfg, q_weight, k_weight)
     table_len = _table_len(cfg, cos_sin)
     if positions is not None:
-        _check_vector(positions, "positions", torch.int32, n)
-    device = q.device
-    _check_devices(device, (q, "q"), (k, "k"), (q_weight, "q_weight"), (k_weight, "k_weight"),
-                   (positions, "positions"), (cos_sin, "cos_sin"), (q_out, "q_out"), (k_out, "k_out"))
-    where, s = _on(device, stream)
-    with where:
-        _lq._check(_lq.load_library().lq_qk_norm_rotate(
-            cfg._ref, _p(q), q_stride, _p(k), k_stride, _p(q_weight), _p(k_weight), _p(positions),
-            _p(cos_sin), table_len, n, _p(q_out), _p(k_out), s), "lq_qk_norm_rotate")
+        _check_vector(positions, "positions", _i32, n)
+    dev = _check_devices(q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out)
+    _call(dev, "lq_qk_norm_rotate", cfg._ref, _p(q), q_stride, _p(k), k_stride, _p(q_weight),
+          _p(k_weight), _p(positions), _p(cos_sin), table_len, n, _p(q_out), _p(k_out),
+          _stream_on(dev, stream))
 
 
 def lq_kv_append(cfg: AttnConfig, cache: KvCache, pos, cu_tokens, q, k, v, q_weight, k_weight, cos_sin,
@@ -265,16 +280,10 @@ def lq_kv_append(cfg: AttnConfig, cache: KvCache, pos, cu_tokens, q, k, v, q_wei
     _check_weights(cfg, q_weight, k_weight)
     table_len = _table_len(cfg, cos_sin)
     _check_places(cache, pos, cu_tokens, n)
-    device = cache.device
-    _check_devices(device, (cache.k_pages, "cache"), (q, "q"), (k, "k"), (v, "v"),
-                   (q_weight, "q_weight"), (k_weight, "k_weight"), (pos, "pos"),
-                   (cu_tokens, "cu_tokens"), (cos_sin, "cos_sin"), (q_out, "q_out"))
-    where, s = _on(device, stream)
-    with where:
-        _lq._check(_lq.load_library().lq_kv_append(
-            cfg._ref, cache._ref, _p(pos), _p(cu_tokens), n, _p(q), q_stride, _p(k), k_stride, _p(v),
-            v_stride, _p(q_weight), _p(k_weight), _p(cos_sin), table_len, _p(q_out), s),
-            "lq_kv_append")
+    dev = _check_devices(cache.k_pages, q, k, v, q_weight, k_weight, pos, cu_tokens, cos_sin, q_out)
+    _call(dev, "lq_kv_append", cfg._ref, cache._ref, _p(pos), _p(cu_tokens), n, _p(q), q_stride, _p(k),
+          k_stride, _p(v), v_stride, _p(q_weight), _p(k_weight), _p(cos_sin), table_len, _p(q_out),
+          _stream_on(dev, stream))
 
 
 def lq_attn_workspace_bytes(cfg: AttnConfig, batch: int) -> int:
@@ -288,30 +297,24 @@ def lq_attn_decode(cfg: AttnConfig, cache: KvCache, pos, q, o, workspace="auto",
     cached tokens: q and o [batch, q_heads, head_dim].  workspace: "auto"
     allocates (torch) what lq_attn_workspace_bytes gives; a CUDA tensor is
     used as it is and must not serve two calls at once."""
-    import torch
     _check_cache(cfg, cache)
     _check_out(q, "q", cfg, cache.batch, cfg.q_heads)
     _check_out(o, "o", cfg, cache.batch, cfg.q_heads)
-    _check_places(cache, pos, None, cache.batch)
-    device = cache.device
-    _check_devices(device, (cache.k_pages, "cache"), (pos, "pos"), (q, "q"), (o, "o"))
+    _check_vector(pos, "pos", _i32, cache.batch)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError(f"workspace: {workspace!r}")
+        dev = _check_devices(cache.k_pages, pos, q, o)
+        # allocated on the call's own stream: the memory is that stream's
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            workspace = torch.empty(max(lq_attn_workspace_bytes(cfg, cache.batch), 0),
+                                    dtype=torch.uint8, device="cuda")
     elif not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
     else:
-        _check_devices(device, (workspace, "workspace"))
-    where, s = _on(device, stream)
-    with where:
-        if isinstance(workspace, str):
-            # allocated on the call's own stream: the memory is that stream's
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(max(lq_attn_workspace_bytes(cfg, cache.batch), 0),
-                                        dtype=torch.uint8, device=device)
-        _lq._check(_lq.load_library().lq_attn_decode(
-            cfg._ref, cache._ref, _p(pos), _p(q), _p(o), _p(workspace),
-            workspace.numel() * workspace.element_size(), s), "lq_attn_decode")
+        dev = _check_devices(cache.k_pages, pos, q, o, workspace)
+    _call(dev, "lq_attn_decode", cfg._ref, cache._ref, _p(pos), _p(q), _p(o), _p(workspace),
+          workspace.numel() * workspace.element_size(), _stream_on(dev, stream))
 
 
 def lq_attn_prefill(cfg: AttnConfig, cache: KvCache, pos, cu_tokens, q, o, stream=None) -> None:
@@ -324,10 +327,6 @@ def lq_attn_prefill(cfg: AttnConfig, cache: KvCache, pos, cu_tokens, q, o, strea
     _check_out(q, "q", cfg, n, cfg.q_heads)
     _check_out(o, "o", cfg, n, cfg.q_heads)
     _check_places(cache, pos, cu_tokens, n)
-    device = cache.device
-    _check_devices(device, (cache.k_pages, "cache"), (pos, "pos"), (cu_tokens, "cu_tokens"), (q, "q"),
-                   (o, "o"))
-    where, s = _on(device, stream)
-    with where:
-        _lq._check(_lq.load_library().lq_attn_prefill(
-            cfg._ref, cache._ref, _p(pos), _p(cu_tokens), n, _p(q), _p(o), s), "lq_attn_prefill")
+    dev = _check_devices(cache.k_pages, pos, cu_tokens, q, o)
+    _call(dev, "lq_attn_prefill", cfg._ref, cache._ref, _p(pos), _p(cu_tokens), n, _p(q), _p(o),
+          _stream_on(dev, stream))

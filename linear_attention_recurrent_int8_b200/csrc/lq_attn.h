@@ -24,7 +24,7 @@ struct RowsArgs {
     // append
     void *k_pages, *v_pages;
     const int32_t *block_table, *pos, *cu;
-    int B, num_pages, page_size, max_pages;
+    int B, num_pages, page_size, page_shift, max_pages;
     int tokens, Hq, Hkv;
     int norm, rot, table_len;
     float eps;

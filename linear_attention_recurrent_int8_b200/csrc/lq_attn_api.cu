@@ -46,6 +46,12 @@ lq_status check_cache(const lq_attn_config *c, const lq_kv_cache *k) {
     return LQ_OK;
 }
 
+int page_shift(const lq_kv_cache *k) {
+    int s = 0;
+    while ((1 << s) < k->page_size) ++s;
+    return s;
+}
+
 // A token-strided [tokens, heads, D] input.
 lq_status check_rows(const lq_attn_config *c, const void *x, int64_t stride, int heads) {
     if (!x) return LQ_ERR_INVALID_ARGUMENT;
@@ -99,7 +105,7 @@ lq::AttnArgs attn_args(const lq_attn_config *c, const lq_kv_cache *k, const int3
     a.Hkv = c->kv_heads;
     a.num_pages = k->num_pages;
     a.page_size = k->page_size;
-    while ((1 << a.page_shift) < k->page_size) ++a.page_shift;
+    a.page_shift = page_shift(k);
     a.max_pages = k->max_pages;
     a.window = c->window;
     a.scale = c->scale;
@@ -194,6 +200,7 @@ lq_status lq_kv_append(const lq_attn_config *cfg, const lq_kv_cache *cache, cons
     a.B = cache->batch;
     a.num_pages = cache->num_pages;
     a.page_size = cache->page_size;
+    a.page_shift = page_shift(cache);
     a.max_pages = cache->max_pages;
     return rows_launch(cfg, a, true, stream);
 }

@@ -53,14 +53,28 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// cap tanh(s / cap), in units of log2.  For BF16 outputs by
-// tanh x = 1 - 2 / (1 + e^{2x}), whose absolute error is a few FP32 steps of
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// cap tanh(scale s / cap) in units of log2.  For BF16 outputs by
+// tanh y = 1 - 2 / (1 + e^{2y}), whose absolute error is a few FP32 steps of
 // cap: far below a BF16 step of any output.  FP32 outputs take tanhf.
+struct SoftCap {
+    float in, out;  // 2 log2(e) scale / cap (BF16) or scale / cap (FP32), and log2(e) cap
+};
+
 template <bool BF16>
-__device__ __forceinline__ float capped_log2(float s, float scale, float cap) {
-    const float x = s * scale / cap;
-    if constexpr (BF16) return cap * kLog2e * (1.0f - __fdividef(2.0f, 1.0f + ex2(2.0f * kLog2e * x)));
-    else return cap * tanhf(x) * kLog2e;
+__device__ __forceinline__ SoftCap soft_cap(float scale, float cap) {
+    return SoftCap{(BF16 ? 2.0f * kLog2e : 1.0f) * scale / cap, kLog2e * cap};
+}
+
+template <bool BF16>
+__device__ __forceinline__ float capped_log2(float s, const SoftCap &c) {
+    if constexpr (BF16) return fmaf(-2.0f * c.out, rcp(1.0f + ex2(s * c.in)), c.out);
+    else return c.out * tanhf(s * c.in);
 }
 
 // Programmatic dependent launch: lets the next launch of the stream start,

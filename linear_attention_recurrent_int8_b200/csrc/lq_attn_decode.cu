@@ -178,6 +178,7 @@ struct Bf16Core {
             }
         }
         const bool part = tok0 + 16 > len || tok0 < lo;
+        const SoftCap cap = soft_cap<true>(a.scale, a.softcap);
         float mx[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -187,7 +188,7 @@ struct Bf16Core {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float &x = s[j][2 * r + e];
-                    x = a.softcap > 0.0f ? capped_log2<true>(x, a.scale, a.softcap) : x * (a.scale * kLog2e);
+                    x = a.softcap > 0.0f ? capped_log2<true>(x, cap) : x * (a.scale * kLog2e);
                     const int tok = tok0 + 8 * j + 2 * t + e;
                     if (part && (tok < lo || tok >= len)) x = -INFINITY;
                     mx[r] = fmaxf(mx[r], x);
@@ -368,11 +369,12 @@ struct F32Core {
             }
         }
         const bool seen = tok0 + tok >= lo && tok0 + tok < len;
+        const SoftCap cap = soft_cap<false>(a.scale, a.softcap);
         bool grew = false;
         float mx[NRL];
 #pragma unroll
         for (int r = 0; r < NRL; ++r) {
-            s[r] = a.softcap > 0.0f ? capped_log2<false>(s[r], a.scale, a.softcap) : s[r] * (a.scale * kLog2e);
+            s[r] = a.softcap > 0.0f ? capped_log2<false>(s[r], cap) : s[r] * (a.scale * kLog2e);
             if (!seen) s[r] = -INFINITY;
             mx[r] = group_max<TOK>(s[r]);
             grew = grew || mx[r] > m[r];

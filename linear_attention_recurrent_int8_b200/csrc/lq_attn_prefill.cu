@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(256) attn_prefill_simt(const AttnArgs a) {
     const int p0 = qt.start + qt.first;               // position of row 0
     const int len = p0 + qt.rows;                     // keys any row sees: [lo, len)
     const int lo = a.window > 0 && p0 + 1 > a.window ? p0 + 1 - a.window : 0;
+    const SoftCap cap = soft_cap<false>(a.scale, a.softcap);
     float o[4][D / 16], m[4], l[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(256) attn_prefill_simt(const AttnArgs a) {
             for (int j = 0; j < NC; ++j) {
                 const int tok = k0 + cg + 16 * j;
                 const bool seen = tok <= p && (a.window == 0 || tok > p - a.window);
-                float x = a.softcap > 0.0f ? capped_log2<false>(s[r][j], a.scale, a.softcap) : s[r][j] * (a.scale * kLog2e);
+                float x = a.softcap > 0.0f ? capped_log2<false>(s[r][j], cap) : s[r][j] * (a.scale * kLog2e);
                 s[r][j] = seen ? x : -INFINITY;
                 mx = fmaxf(mx, s[r][j]);
             }
@@ -406,6 +407,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         // scores enter as 2^(c x): c = log2(e) |scale| (never 0, so that a
         // masked score stays -inf), or 1 for capped scores
         const float c = CAP ? 1.0f : fmaxf(fabsf(a.scale * kLog2e), 1e-30f);
+        const SoftCap cap = soft_cap<true>(a.scale, a.softcap);
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int j = 0; j < n; ++j) {
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             tmem_load_row(sa, x);
             if constexpr (CAP) {
 #pragma unroll
-                for (int i = 0; i < KT; ++i) x[i] = capped_log2<true>(x[i], a.scale, a.softcap);
+                for (int i = 0; i < KT; ++i) x[i] = capped_log2<true>(x[i], cap);
             } else if (a.scale < 0.0f) {
 #pragma unroll
                 for (int i = 0; i < KT; ++i) x[i] = -x[i];

@@ -18,91 +18,110 @@
 namespace lq {
 namespace {
 
+// A lane's 8 channels of a row as stored, in two groups of four: channels
+// off0 .. off0 + 3 and off1 .. off1 + 3 (off1 = off0 + 4 unless SPLIT).
 template <bool BF16>
 struct Raw {
-    uint4 w[BF16 ? 1 : 2];
+    uint32_t w[BF16 ? 4 : 8];
 };
 
-template <bool BF16>
-__device__ __forceinline__ Raw<BF16> load_raw(const void *p, size_t i) {
+template <bool BF16, bool SPLIT>
+__device__ __forceinline__ Raw<BF16> load_raw(const void *row, int off0, int off1) {
     Raw<BF16> r;
-    const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + i * (BF16 ? 2 : 4));
-    r.w[0] = s[0];
-    if constexpr (!BF16) r.w[1] = s[1];
+    if constexpr (BF16) {
+        const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(row);
+        if constexpr (SPLIT) {
+            const uint2 a = *reinterpret_cast<const uint2 *>(p + off0), b = *reinterpret_cast<const uint2 *>(p + off1);
+            r.w[0] = a.x, r.w[1] = a.y, r.w[2] = b.x, r.w[3] = b.y;
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4 *>(p + off0);
+            r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+        }
+    } else {
+        const float *p = static_cast<const float *>(row);
+        const uint4 a = *reinterpret_cast<const uint4 *>(p + off0), b = *reinterpret_cast<const uint4 *>(p + off1);
+        r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+        r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
+    }
     return r;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void store_raw(void *p, size_t i, const Raw<BF16> &r) {
-    uint4 *d = reinterpret_cast<uint4 *>(static_cast<char *>(p) + i * (BF16 ? 2 : 4));
-    d[0] = r.w[0];
-    if constexpr (!BF16) d[1] = r.w[1];
+template <bool BF16, bool SPLIT>
+__device__ __forceinline__ void store_raw(void *row, int off0, int off1, const Raw<BF16> &r) {
+    if constexpr (BF16) {
+        __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(row);
+        if constexpr (SPLIT) {
+            *reinterpret_cast<uint2 *>(p + off0) = make_uint2(r.w[0], r.w[1]);
+            *reinterpret_cast<uint2 *>(p + off1) = make_uint2(r.w[2], r.w[3]);
+        } else {
+            *reinterpret_cast<uint4 *>(p + off0) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        }
+    } else {
+        float *p = static_cast<float *>(row);
+        *reinterpret_cast<uint4 *>(p + off0) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        *reinterpret_cast<uint4 *>(p + off1) = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
+    }
 }
 
 template <bool BF16>
 __device__ __forceinline__ void unpack(const Raw<BF16> &r, float (&x)[8]) {
 #pragma unroll
-    for (int j = 0; j < (BF16 ? 1 : 2); ++j) {
-        const uint32_t w[4] = {r.w[j].x, r.w[j].y, r.w[j].z, r.w[j].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if constexpr (BF16) {
-                x[2 * e] = __uint_as_float(w[e] << 16);
-                x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-            } else {
-                x[4 * j + e] = __uint_as_float(w[e]);
-            }
-        }
+    for (int e = 0; e < 8; ++e) {
+        if constexpr (BF16) x[e] = __uint_as_float((e & 1) ? (r.w[e / 2] & 0xFFFF0000u) : (r.w[e / 2] << 16));
+        else x[e] = __uint_as_float(r.w[e]);
     }
 }
 
 template <bool BF16>
 __device__ __forceinline__ Raw<BF16> pack(const float (&x)[8]) {
     Raw<BF16> r;
-    if constexpr (BF16) {
-        uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-            w[e] = *reinterpret_cast<const uint32_t *>(&p);
-        }
-        r.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-        r.w[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-        r.w[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+    for (int e = 0; e < 8; ++e) {
+        if constexpr (BF16) {
+            if ((e & 1) == 0) {
+                const __nv_bfloat162 p = __floats2bfloat162_rn(x[e], x[e + 1]);
+                r.w[e / 2] = *reinterpret_cast<const uint32_t *>(&p);
+            }
+        } else r.w[e] = __float_as_uint(x[e]);
     }
     return r;
 }
 
-template <int N>
-__device__ __forceinline__ void load_f32(float *v, const float *p) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        const float4 x = __ldg(reinterpret_cast<const float4 *>(p + i));
-        v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
-    }
+__device__ __forceinline__ void load4(float *v, const float *p) {
+    const float4 x = __ldg(reinterpret_cast<const float4 *>(p));
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
 }
 
 // One block: NR rows for each of its groups of D / 8 lanes, all of token
 // blockIdx.x; rows are the q heads, the k heads and, when appending, the v
-// heads (copied).
-template <int D, bool BF16, bool ADJ, bool APPEND, int NR>
-__global__ void __launch_bounds__(256) rows_kernel(const RowsArgs a) {
+// heads (copied).  SPLIT (rotation by halves): the lanes of the rotated
+// channels hold 4 of the first half and their 4 partners of the second, so
+// that a pair needs no exchange and its cosine and sine are loaded once.
+template <int D, bool BF16, bool SPLIT, bool APPEND, int NR>
+__global__ void __launch_bounds__(256, NR == 4 ? 4 : 6) rows_kernel(const RowsArgs a) {
     constexpr int L = D / 8;
-    const int tid = threadIdx.x, l = tid & (L - 1), c = 8 * l;
+    const int tid = threadIdx.x, l = tid & (L - 1);
+    const int half = a.rot / 2;
+    const bool turned = 8 * l < a.rot;
+    const int off0 = SPLIT && turned ? 4 * l : 8 * l;
+    const int off1 = SPLIT && turned ? half + 4 * l : 8 * l + 4;
     const int groups = blockDim.x / L;
     const long long t = blockIdx.x;
     const int R = a.Hq + a.Hkv * (APPEND ? 2 : 1);
     const int r0 = blockIdx.y * groups * NR + tid / L;
+    constexpr int es = BF16 ? 2 : 4;
 
+    const char *qrow = static_cast<const char *>(a.q) + t * a.q_stride * es;
+    const char *krow = static_cast<const char *>(a.k) + t * a.k_stride * es;
+    const char *vrow = APPEND ? static_cast<const char *>(a.v) + t * a.v_stride * es : nullptr;
     Raw<BF16> raw[NR];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const int r = r0 + i * groups;
-        if (r >= R) raw[i] = Raw<BF16>{};
-        else if (r < a.Hq) raw[i] = load_raw<BF16>(a.q, t * a.q_stride + r * D + c);
-        else if (!APPEND || r < a.Hq + a.Hkv) raw[i] = load_raw<BF16>(a.k, t * a.k_stride + (r - a.Hq) * D + c);
-        else raw[i] = load_raw<BF16>(a.v, t * a.v_stride + (r - a.Hq - a.Hkv) * D + c);
+        const char *row = r < a.Hq ? qrow + r * (D * es) : krow + (r - a.Hq) * (D * es);
+        if (APPEND && r >= a.Hq + a.Hkv) row = vrow + (r - a.Hq - a.Hkv) * (D * es);
+        raw[i] = Raw<BF16>{};
+        if (r < R) raw[i] = load_raw<BF16, SPLIT>(row, off0, off1);
     }
 
     // the token's position and, when appending, its place in the cache
@@ -130,15 +149,15 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsArgs a) {
         const int first = __ldg(a.pos + b);
         if (first < 0) return;  // idle slot
         p = first + i;
-        bool bad_pos = i < 0 || p >= (long long)a.max_pages * a.page_size || (a.rot > 0 && p >= a.table_len);
+        const bool bad_pos = i < 0 || p >= (long long)a.max_pages * a.page_size || (a.rot > 0 && p >= a.table_len);
         int page = 0;
-        if (!bad_pos) page = __ldg(a.block_table + (size_t)b * a.max_pages + (int)(p / a.page_size));
+        if (!bad_pos) page = __ldg(a.block_table + (size_t)b * a.max_pages + (int)(p >> a.page_shift));
         const bool bad_page = page < 0 || page >= a.num_pages;
         if (bad_pos || bad_page) {
             if (tid == 0 && blockIdx.y == 0) atomicOr(&g_dev_error, bad_pos ? kErrBadPosition : kErrBadPage);
             return;
         }
-        page_row = (size_t)page * a.Hkv * a.page_size + (size_t)(p % a.page_size);
+        page_row = (size_t)page * a.Hkv * a.page_size + (size_t)(p & (a.page_size - 1));
     } else if (a.positions) {
         p = __ldg(a.positions + t);
         if (p < 0) return;  // padding
@@ -148,18 +167,12 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsArgs a) {
         }
     }
 
-    const int half = a.rot / 2;
-    const bool turned = c < a.rot;
-    // rot is a multiple of 16, so a lane's 8 channels lie on one side of
-    // rot / 2 and the partner channels belong to one other lane
-    const bool low = c < half;
-    const int partner = turned ? (low ? l + half / 8 : l - half / 8) : l;
-    constexpr int NT = ADJ ? 4 : 8;
-    float cs[NT], sn[NT];
+    // the lane's four pairs: (x[e], x[4 + e]) when split, else (x[2 e], x[2 e + 1])
+    float cs[4], sn[4];
     if (turned) {
-        const float *row = a.cos_sin + (size_t)p * a.rot + (ADJ ? c / 2 : (low ? c : c - half));
-        load_f32<NT>(cs, row);
-        load_f32<NT>(sn, row + half);
+        const float *row = a.cos_sin + (size_t)p * a.rot + 4 * l;
+        load4(cs, row);
+        load4(sn, row + half);
     }
 
 #pragma unroll
@@ -173,48 +186,41 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
             ss = group_sum<L>(ss);
-            const float f = 1.0f / sqrtf(a.norm == 2 ? ss * (1.0f / D) + a.eps : ss + a.eps);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= f;
+            const float f = rsqrtf(a.norm == 2 ? fmaf(ss, 1.0f / D, a.eps) : ss + a.eps);
             const float *w = r < a.Hq ? a.q_weight : a.k_weight;
-            if (w && !is_v) {
+            if (w) {
                 float wv[8];
-                load_f32<8>(wv, w + c);
+                load4(wv, w + off0);
+                load4(wv + 4, w + off1);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= wv[e];
+                for (int e = 0; e < 8; ++e) x[e] = x[e] * f * wv[e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= f;
             }
         }
-        if (a.rot > 0) {
-            if constexpr (ADJ) {
-                if (turned) {
+        if (turned) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x0 = x[2 * e], x1 = x[2 * e + 1];
-                        x[2 * e] = x0 * cs[e] - x1 * sn[e];
-                        x[2 * e + 1] = x1 * cs[e] + x0 * sn[e];
-                    }
-                }
-            } else {
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], partner, L);
-                if (turned) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = low ? x[e] * cs[e] - y[e] * sn[e] : x[e] * cs[e] + y[e] * sn[e];
-                }
+            for (int e = 0; e < 4; ++e) {
+                float &x0 = x[SPLIT ? e : 2 * e], &x1 = x[SPLIT ? e + 4 : 2 * e + 1];
+                const float y0 = x0 * cs[e] - x1 * sn[e];
+                x1 = x1 * cs[e] + x0 * sn[e];
+                x0 = y0;
             }
         }
         if (r >= R) continue;
         const Raw<BF16> out = is_v ? raw[i] : pack<BF16>(x);
-        if (r < a.Hq) store_raw<BF16>(a.q_out, ((size_t)t * a.Hq + r) * D + c, out);
+        char *dst;
+        if (r < a.Hq) dst = static_cast<char *>(a.q_out) + ((size_t)t * a.Hq + r) * (D * es);
         else if constexpr (APPEND) {
             const int h = is_v ? r - a.Hq - a.Hkv : r - a.Hq;
-            store_raw<BF16>(is_v ? a.v_pages : a.k_pages, (page_row + (size_t)h * a.page_size) * D + c, out);
-        } else store_raw<BF16>(a.k_out, ((size_t)t * a.Hkv + (r - a.Hq)) * D + c, out);
+            dst = static_cast<char *>(is_v ? a.v_pages : a.k_pages) + (page_row + (size_t)h * a.page_size) * (D * es);
+        } else dst = static_cast<char *>(a.k_out) + ((size_t)t * a.Hkv + (r - a.Hq)) * (D * es);
+        store_raw<BF16, SPLIT>(dst, off0, off1, out);
     }
 }
 
-template <int D, bool BF16, bool ADJ, bool APPEND>
+template <int D, bool BF16, bool SPLIT, bool APPEND>
 cudaError_t launch_rows_d(const RowsArgs &a, cudaStream_t stream) {
     constexpr int L = D / 8;
     const int R = a.Hq + a.Hkv * (APPEND ? 2 : 1);
@@ -225,14 +231,14 @@ cudaError_t launch_rows_d(const RowsArgs &a, cudaStream_t stream) {
     threads = threads >= 256 ? 256 : (threads + 31) / 32 * 32;
     const int rows = threads / L * nr;
     const dim3 grid((unsigned)a.tokens, (unsigned)((R + rows - 1) / rows));
-    if (wide) rows_kernel<D, BF16, ADJ, APPEND, 4><<<grid, threads, 0, stream>>>(a);
-    else rows_kernel<D, BF16, ADJ, APPEND, 1><<<grid, threads, 0, stream>>>(a);
+    if (wide) rows_kernel<D, BF16, SPLIT, APPEND, 4><<<grid, threads, 0, stream>>>(a);
+    else rows_kernel<D, BF16, SPLIT, APPEND, 1><<<grid, threads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
 template <int D, bool BF16>
-cudaError_t launch_rows_t(const RowsArgs &a, bool adjacent, bool append, cudaStream_t stream) {
-    if (adjacent)
+cudaError_t launch_rows_t(const RowsArgs &a, bool split, bool append, cudaStream_t stream) {
+    if (split)
         return append ? launch_rows_d<D, BF16, true, true>(a, stream) : launch_rows_d<D, BF16, true, false>(a, stream);
     return append ? launch_rows_d<D, BF16, false, true>(a, stream) : launch_rows_d<D, BF16, false, false>(a, stream);
 }
@@ -240,10 +246,11 @@ cudaError_t launch_rows_t(const RowsArgs &a, bool adjacent, bool append, cudaStr
 }  // namespace
 
 cudaError_t launch_rows(const RowsArgs &a, int D, bool bf16, bool adjacent, bool append, cudaStream_t stream) {
+    const bool split = a.rot > 0 && !adjacent;
     switch (D) {
-        case 64: return bf16 ? launch_rows_t<64, true>(a, adjacent, append, stream) : launch_rows_t<64, false>(a, adjacent, append, stream);
-        case 128: return bf16 ? launch_rows_t<128, true>(a, adjacent, append, stream) : launch_rows_t<128, false>(a, adjacent, append, stream);
-        case 256: return bf16 ? launch_rows_t<256, true>(a, adjacent, append, stream) : launch_rows_t<256, false>(a, adjacent, append, stream);
+        case 64: return bf16 ? launch_rows_t<64, true>(a, split, append, stream) : launch_rows_t<64, false>(a, split, append, stream);
+        case 128: return bf16 ? launch_rows_t<128, true>(a, split, append, stream) : launch_rows_t<128, false>(a, split, append, stream);
+        case 256: return bf16 ? launch_rows_t<256, true>(a, split, append, stream) : launch_rows_t<256, false>(a, split, append, stream);
     }
     return cudaErrorInvalidValue;
 }
