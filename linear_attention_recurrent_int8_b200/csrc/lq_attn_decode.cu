@@ -580,11 +580,11 @@ __global__ void __launch_bounds__(Tile<D, BF16>::kWarps * 32, 1)
             whole = c.t == 0;
             fresh = false;
         }
-        if (!mbar_wait_bounded(full + st, ph)) {
+        if (!bar_wait(full + st, ph)) {
             // give the copies still in flight their time before the block's shared memory is freed
             for (int k = i + 1; k < filled; ++k) {
                 if (++st == pl.stages) st = 0, ph ^= 1;
-                mbar_wait_bounded(full + st, ph);
+                bar_wait(full + st, ph);
             }
             return;
         }

@@ -171,7 +171,8 @@ cudaError_t launch_simt(const AttnArgs &a, cudaStream_t stream) {
 // BF16: tensor cores
 // ---------------------------------------------------------------------------
 
-// 128 consecutive TMEM columns of the warp's 32 lanes; the wait is part of the statement.
+// A row of 128 or 64 consecutive TMEM columns for each of the warp's 32 lanes;
+// the wait is part of the statement.
 __device__ __forceinline__ void tmem_load_row(uint32_t taddr, float (&v)[128]) {
     uint32_t r[128];
     asm volatile(
@@ -185,44 +186,136 @@ __device__ __forceinline__ void tmem_load_row(uint32_t taddr, float (&v)[128]) {
 }
 __device__ __forceinline__ void tmem_load_row(uint32_t taddr, float (&v)[64]) { tmem_load64(taddr, v); }
 
-// D (TMEM) = A (TMEM) B (+ D when `accumulate`), BF16, issued by one thread.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            bool accumulate) {
+__device__ __forceinline__ void tmem_store_row(uint32_t taddr, const float (&v)[32]) { tmem_store32(taddr, v); }
+__device__ __forceinline__ void tmem_store_row(uint32_t taddr, const float (&v)[16]) {
     asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
         : "memory");
 }
 
-// Shared-memory descriptor of an MN-major operand stored with the 128-byte
-// swizzle: blocks of 64 MN elements (128 bytes) by K rows, 8 K rows to an
-// atom of 1024 bytes (the stride byte offset), `block` bytes from one block
-// of 64 MN elements to the next (the leading byte offset).
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t block) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((block >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Two FP32 values in one 64-bit register: one instruction for both.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 two(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void apart(f32x2 v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// Maximum of three that keeps NaN.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// 2^v of two values on the FMA pipe, for the weights that the special
+// function unit has no time for: v = n + r with n the nearest integer (left
+// in the low bits by adding 1.5 * 2^23) and |r| <= 1/2, 2^r by a cubic
+// through 1 (least maximum relative error, 1.0e-4: a fortieth of the BF16
+// rounding that follows), n added to the exponent.  From -127 down: 0.
+// v <= 127.
+__device__ __forceinline__ void ex2_fma(f32x2 v, float &a, float &b) {
+    float x, y;
+    apart(v, x, y);
+    v = two(fmaxf(x, -127.0f), fmaxf(y, -127.0f));
+    const f32x2 magic = two(12582912.0f, 12582912.0f), one = two(1.0f, 1.0f);
+    const f32x2 t = add2(v, magic), n = add2(t, two(-12582912.0f, -12582912.0f));
+    const f32x2 r = fma2(n, two(-1.0f, -1.0f), v);
+    f32x2 p = fma2(r, two(0.05500893294811249f, 0.05500893294811249f), two(0.2422109693288803f, 0.2422109693288803f));
+    p = fma2(p, r, two(0.6932829022407532f, 0.6932829022407532f));
+    p = fma2(p, r, one);
+    float pa, pb, ta, tb;
+    apart(p, pa, pb);
+    apart(t, ta, tb);
+    a = __int_as_float(__float_as_int(pa) + (int)((unsigned)__float_as_int(ta) << 23));
+    b = __int_as_float(__float_as_int(pb) + (int)((unsigned)__float_as_int(tb) << 23));
+}
+
+// tanh y of two values, |y| <= 1: y + y^3 times a cubic in y^2 (least maximum
+// error, 4.1e-6).
+__device__ __forceinline__ f32x2 tanh_fma(f32x2 y) {
+    const f32x2 u = mul2(y, y);
+    f32x2 p = fma2(u, two(0.008854211308062077f, 0.008854211308062077f), two(-0.04448200762271881f, -0.04448200762271881f));
+    p = fma2(p, u, two(0.13020214438438416f, 0.13020214438438416f));
+    p = fma2(p, u, two(-0.3329765796661377f, -0.3329765796661377f));
+    return fma2(mul2(y, u), p, y);
+}
+
+// Shared-memory operand descriptors as two words: all K steps of a tile share
+// the upper word and add to the lower one.  K-major, 128-byte swizzle: 8-row
+// atoms of 1024 bytes (the stride byte offset).  MN-major, 128-byte swizzle:
+// blocks of 64 MN elements (128 bytes) by K rows, 8 K rows to an atom of 1024
+// bytes, `block` bytes from one block to the next (the leading byte offset).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t block) { return (saddr >> 4) | (block >> 4) << 16; }
+
+// D (TMEM) = A B (+ D when `add`), BF16, issued by one thread; A from shared
+// memory or, with its weights, from TMEM.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{ .reg .pred p; .reg .b64 da, db; setp.ne.b32 p, %4, 0; mov.b64 da, {%1, %5}; mov.b64 db, {%2, %5}; "
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p; }" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "n"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{ .reg .pred p; .reg .b64 db; setp.ne.b32 p, %4, 0; mov.b64 db, {%2, %5}; "
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p; }" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "n"(kDescHi)
+        : "memory");
+}
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
 }
 
 template <int D>
 struct Tc {
     static constexpr int kStreams = D == 256 ? 1 : 2;     // query tiles of 128 rows
-    static constexpr int kKeys = D == 256 ? 64 : 128;     // keys of a tile
+    static constexpr int kKeys = D == 128 ? 128 : 64;     // keys of a tile
+    static constexpr int kTiles = D == 128 ? 1 : 2;       // score tiles of a stream in TMEM
     static constexpr int kHalves = D / 64;                // 128-byte column blocks
     static constexpr int kQBytes = 128 * D * 2;           // a query tile
     static constexpr int kSlotBytes = kKeys * D * 2;      // a tile of K or V
-    static constexpr int kSlots = (kStreams * kQBytes + 5 * kSlotBytes) <= 225 * 1024 ? 5 : 4;
+    static constexpr int kSlots = 5;
     static constexpr int kSoftWarps = 4 * kStreams;
     static constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
     static constexpr int kThreads = (kSoftWarps + 2) * 32;
     static constexpr int kSmem = 1024 + kStreams * kQBytes + kSlots * kSlotBytes;
-    // TMEM columns: scores (two tiles: one per stream, or two of one stream),
-    // whose first half the weights overwrite, then the outputs
+    // of 8 pairs of weights, those exponentiated on the FMA pipe
+    static constexpr int kFmaOf8 = 2;
+    // TMEM columns: the score tiles, whose first half the weights overwrite,
+    // then the outputs
     static constexpr uint32_t kColS = 0, kColO = 256;
+    static constexpr uint32_t kCols = 512;
 };
 
 struct TcBars {
-    uint64_t q_full, kv_full[5], kv_empty[5], s_full[2], p_ready[2], o_done[2], tail;
+    uint64_t q_full, kv_full[5], kv_empty[5], s_full[4], p_half[2], p_ready[2], o_done[2], tail;
 };
 
 // One block: 128 kStreams rows, each a (token, head) pair of `group` heads
@@ -247,19 +340,25 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     const int h0 = blockIdx.y << group_shift, kv = h0 / (a.Hq / a.Hkv);
     const int p0 = qt.start + qt.first, len = p0 + qt.rows;  // keys any row sees: lo .. len - 1
     const int lo = a.window > 0 && p0 + 1 > a.window ? p0 + 1 - a.window : 0;
+    // (a second stream without rows is left out)
+    const int streams = NS == 2 && qt.rows > tokens / 2 ? 2 : 1;
     const int k_first = lo / KT, n = (len - 1) / KT - k_first + 1;
 
     if (tid == 0) {
         mbar_init(&bars.q_full, 1);
         for (int i = 0; i < T::kSlots; ++i) mbar_init(&bars.kv_full[i], 1), mbar_init(&bars.kv_empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&bars.s_full[i], 1), mbar_init(&bars.p_ready[i], 4), mbar_init(&bars.o_done[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.s_full[2 * i], 1), mbar_init(&bars.s_full[2 * i + 1], 1);
+            mbar_init(&bars.o_done[i], 1);
+            mbar_init(&bars.p_half[i], 4), mbar_init(&bars.p_ready[i], 4);
+        }
         mbar_init(&bars.tail, 1);
     }
-    if (warp == T::kMmaWarp) tmem_alloc(&tmem_slot, 512);
+    if (warp == T::kMmaWarp) tmem_alloc(&tmem_slot, T::kCols);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tm = tmem_slot;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
     if (warp == T::kLoadWarp) {
         // ------------------------------------------------------------ TMA
@@ -270,12 +369,29 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                 for (int x = 0; x < NH; ++x)
                     tma_page_load(qs + s * T::kQBytes + x * 16384, &qmap, 64 * x, h0, t0 + s * per, &bars.q_full);
         }
+        // lane = (box of rows, column block) of a tile; boxes past the
+        // visible keys are filled with zeros
         const int box_rows = 1 << box_shift, boxes = KT >> box_shift;
+        const bool mine = lane < boxes * NH;
+        const int bx = lane / NH, x = lane - bx * NH;
         int slot = 0, use = 0, tail_phase = 0;
-        bool ok = true;
+        auto visible = [&](int j) {
+            const int tok = (k_first + j) * KT + bx * box_rows;
+            return mine && tok < len && tok + box_rows > lo;
+        };
+        // the block table is read a tile ahead of its use
+        auto page_of = [&](int j) {
+            const int tok = (k_first + j) * KT + bx * box_rows;
+            return visible(j) ? __ldg(a.block_table + (size_t)qt.b * a.max_pages + (tok >> a.page_shift)) : -1;
+        };
+        auto map_row = [&](int j, int page) -> int {
+            if (page >= 0 && page < a.num_pages) return page * a.Hkv + kv;
+            if (visible(j)) atomicOr(&g_dev_error, kErrBadPage);
+            return -1;
+        };
         // tile j of K or V into the next slot
-        auto load = [&](const CUtensorMap *map, int j, bool is_v) {
-            if (use > 0 && !mbar_wait_bounded(&bars.kv_empty[slot], (use - 1) & 1)) return false;
+        auto load = [&](const CUtensorMap *map, int j, int z, bool is_v) {
+            if (use > 0 && !bar_wait(&bars.kv_empty[slot], (use - 1) & 1)) return false;
             unsigned char *dst = ring + slot * T::kSlotBytes;
             const int k0 = (k_first + j) * KT;
             // V rows that no query row sees may hold NaN, which a weight of
@@ -284,18 +400,11 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             uint64_t *bar = clear ? &bars.tail : &bars.kv_full[slot];
             if (lane == 0) mbar_arrive_expect_tx(bar, T::kSlotBytes);
             __syncwarp();
-            for (int i = lane; i < boxes * NH; i += 32) {
-                const int bx = i / NH, x = i - bx * NH, tok = k0 + bx * box_rows;
-                int z = -1, row = 0;  // boxes past the visible keys are filled with zeros
-                if (tok < len && tok + box_rows > lo) {
-                    const int page = __ldg(a.block_table + (size_t)qt.b * a.max_pages + (tok >> a.page_shift));
-                    if (page >= 0 && page < a.num_pages) z = page * a.Hkv + kv, row = tok & (a.page_size - 1);
-                    else atomicOr(&g_dev_error, kErrBadPage);
-                }
-                tma_page_load(dst + x * (KT * 128) + bx * box_rows * 128, map, 64 * x, row, z, bar);
-            }
+            if (mine)
+                tma_page_load(dst + x * (KT * 128) + bx * box_rows * 128, map, 64 * x,
+                              (k0 + bx * box_rows) & (a.page_size - 1), z, bar);
             if (clear) {
-                if (!mbar_wait_bounded(&bars.tail, tail_phase)) return false;
+                if (!bar_wait(&bars.tail, tail_phase)) return false;
                 tail_phase ^= 1;
                 for (int i = lane; i < KT * D / 8; i += 32) {
                     const int r = i / (D / 8), c = i - r * (D / 8);
@@ -310,91 +419,112 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             return true;
         };
         // in the order the MMA lane takes them
-        ok = load(&kmap, 0, false);
+        int z = map_row(0, page_of(0)), page = page_of(1);
+        bool ok = load(&kmap, 0, z, false);
         for (int j = 0; ok && j < n; ++j) {
-            if (NS == 1 && j + 1 < n) ok = load(&kmap, j + 1, false);
-            if (ok) ok = load(&vmap, j, true);
-            if (NS == 2 && ok && j + 1 < n) ok = load(&kmap, j + 1, false);
+            const int zv = z;
+            if (T::kTiles == 1) ok = load(&vmap, j, zv, true);
+            if (ok && j + 1 < n) {
+                z = map_row(j + 1, page);
+                page = page_of(j + 2);
+                ok = load(&kmap, j + 1, z, false);
+            }
+            if (ok && T::kTiles == 2) ok = load(&vmap, j, zv, true);
         }
     } else if (warp == T::kMmaWarp) {
         // ------------------------------------------------------------ MMAs
-        if (lane == 0) {
-            constexpr uint32_t id_qk = idesc_bf16(128, KT, false, false), id_pv = idesc_bf16(128, D, false, true);
-            int slot = 0, use = 0;
-            auto take = [&](int &at) {
-                at = slot;
-                const bool ok = mbar_wait_bounded(&bars.kv_full[slot], use & 1);
-                if (++slot == T::kSlots) slot = 0, ++use;
-                return ok;
-            };
-            auto qk = [&](int s, int at, uint32_t col) {  // scores of stream s at TMEM column col
-                const uint32_t qa = smem_u32(qs + s * T::kQBytes), ka = smem_u32(ring + at * T::kSlotBytes);
+        // The whole warp runs the loop, so that addresses stay uniform, and
+        // one lane issues: with the loop inside that lane's branch an MMA
+        // took about 90 cycles to issue, and the issue bounded the kernel.
+        constexpr uint32_t id_qk = idesc_bf16(128, KT, false, false), id_pv = idesc_bf16(128, D, false, true);
+        const uint32_t q_desc = desc_k(smem_u32(qs)), ring_addr = smem_u32(ring);
+        int slot = 0, use = 0;
+        auto take = [&](int &at) {
+            at = slot;
+            const bool ok = bar_wait(&bars.kv_full[slot], use & 1);
+            if (++slot == T::kSlots) slot = 0, ++use;
+            return __all_sync(0xffffffffu, ok) != 0;
+        };
+        // scores of one stream into its score tile at column col: the tile's
+        // last weights were read by an earlier MMA of this thread
+        auto qk = [&](int s, int at, uint32_t col) {
+            const uint32_t k_desc = desc_k(ring_addr + at * T::kSlotBytes);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k & 3) * 32;
-                    mma_bf16(tm + col, smem_desc_sw128(qa + (k >> 2) * 16384 + off),
-                             smem_desc_sw128(ka + (k >> 2) * (KT * 128) + off), id_qk, k > 0);
-                }
-            };
-            auto pv = [&](int s, int at, uint32_t col, bool add) {
-                const uint32_t va = smem_u32(ring + at * T::kSlotBytes);
+            for (int k = 0; k < D / 16; ++k)
+                mma_ss(col, q_desc + (s * T::kQBytes + (k >> 2) * 16384 + (k & 3) * 32) / 16,
+                       k_desc + ((k >> 2) * (KT * 128) + (k & 3) * 32) / 16, id_qk, k > 0);
+        };
+        // half of the product with V
+        auto pv = [&](int s, int at, uint32_t col, int half, bool add) {
+            const uint32_t v_desc = desc_mn(ring_addr + at * T::kSlotBytes, KT * 128);
 #pragma unroll
-                for (int k = 0; k < KT / 16; ++k)
-                    mma_bf16_ta(tm + T::kColO + s * D, tm + col + 8 * k, smem_desc_mn_sw128(va + k * 2048, KT * 128), id_pv,
-                                add || k > 0);
-            };
-            bool ok = mbar_wait_bounded(&bars.q_full, 0);
-            int ks = 0, vs = 0;
-            ok = ok && take(ks);
-            if (ok) {
-                tc_fence_after_sync();
-#pragma unroll
-                for (int s = 0; s < NS; ++s) {
-                    qk(s, ks, T::kColS + s * KT);
-                    mma_commit(&bars.s_full[s]);
-                }
-                mma_commit(&bars.kv_empty[ks]);
+            for (int i = 0; i < KT / 32; ++i) {
+                const int k = half * (KT / 32) + i;
+                mma_ts(tm + T::kColO + s * D, col + 8 * k, v_desc + k * (2048 / 16), id_pv, add || i > 0);
             }
-            for (int j = 0; ok && j < n; ++j) {
-                const bool more = j + 1 < n;
-                if constexpr (NS == 2) {
-                    ok = take(vs) && (!more || take(ks));
-                    for (int s = 0; ok && s < 2; ++s) {
-                        ok = mbar_wait_bounded(&bars.p_ready[s], j & 1);
-                        if (!ok) break;
-                        tc_fence_after_sync();
-                        pv(s, vs, T::kColS + s * KT, j > 0);
-                        if (more) {
-                            qk(s, ks, T::kColS + s * KT);
-                            mma_commit(&bars.s_full[s]);
-                        } else {
-                            mma_commit(&bars.o_done[s]);
-                        }
-                    }
-                    if (ok) {
-                        mma_commit(&bars.kv_empty[vs]);
-                        if (more) mma_commit(&bars.kv_empty[ks]);
-                    }
-                } else {
-                    if (more) {
-                        ok = take(ks);
-                        if (!ok) break;
-                        tc_fence_after_sync();
-                        qk(0, ks, T::kColS + ((j + 1) & 1) * KT);
-                        mma_commit(&bars.s_full[(j + 1) & 1]);
-                        mma_commit(&bars.kv_empty[ks]);
-                    }
-                    ok = take(vs) && mbar_wait_bounded(&bars.p_ready[0], j & 1);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    pv(0, vs, T::kColS + (j & 1) * KT, j > 0);
-                    mma_commit(&bars.o_done[0]);
-                    mma_commit(&bars.kv_empty[vs]);
-                }
+        };
+        auto wait = [&](uint64_t *bar, int parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity)) != 0; };
+        int ks = 0, vs = 0;
+        bool ok = wait(&bars.q_full, 0) && take(ks);
+        tc_fence_after_sync();
+        if (ok && elect_one()) {
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                if (s >= streams) break;
+                qk(s, ks, tm + T::kColS + s * T::kTiles * KT);
+                mma_commit(&bars.s_full[s * T::kTiles]);
             }
+            mma_commit(&bars.kv_empty[ks]);
         }
         __syncwarp();
-    } else {
+        for (int j = 0; ok && j < n; ++j) {
+            const bool more = j + 1 < n;
+            if constexpr (T::kTiles == 2) {
+                // two score tiles: the next scores are made during this
+                // tile's softmax
+                if (more) {
+                    ok = take(ks);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int s = 0; s < NS; ++s) {
+                            if (s >= streams) break;
+                            qk(s, ks, tm + T::kColS + (2 * s + ((j + 1) & 1)) * KT);
+                            mma_commit(&bars.s_full[2 * s + ((j + 1) & 1)]);
+                        }
+                        mma_commit(&bars.kv_empty[ks]);
+                    }
+                    __syncwarp();
+                }
+                ok = take(vs);
+            } else {
+                ok = take(vs) && (!more || take(ks));
+            }
+            for (int s = 0; ok && s < streams; ++s) {
+                const uint32_t col = tm + T::kColS + (T::kTiles == 2 ? 2 * s + (j & 1) : s) * KT;
+                ok = wait(&bars.p_half[s], j & 1);
+                if (!ok) break;
+                tc_fence_after_sync();
+                if (elect_one()) pv(s, vs, col, 0, j > 0);
+                __syncwarp();
+                ok = wait(&bars.p_ready[s], j & 1);
+                if (!ok) break;
+                tc_fence_after_sync();
+                if (elect_one()) {
+                    pv(s, vs, col, 1, true);
+                    if (T::kTiles == 2 || !more) mma_commit(&bars.o_done[s]);
+                    if (s + 1 == streams) mma_commit(&bars.kv_empty[vs]);
+                    if (T::kTiles == 1 && more) {
+                        qk(s, ks, col);
+                        mma_commit(&bars.s_full[s]);
+                        if (s + 1 == streams) mma_commit(&bars.kv_empty[ks]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp < 4 * streams) {
         // ------------------------------------------------------------ softmax: one row per thread
         const int s = warp >> 2, q4 = warp & 3;
         const int R = s * 128 + 32 * q4 + lane;
@@ -408,18 +538,30 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         // masked score stays -inf), or 1 for capped scores
         const float c = CAP ? 1.0f : fmaxf(fabsf(a.scale * kLog2e), 1e-30f);
         const SoftCap cap = soft_cap<true>(a.scale, a.softcap);
+        const float cap_in = a.scale / a.softcap, in_reach = 1.0f / fabsf(cap_in);
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int j = 0; j < n; ++j) {
-            const int buf = NS == 2 ? s : (j & 1);
+            const int buf = T::kTiles == 2 ? 2 * s + (j & 1) : s;
             const uint32_t sa = lanes + T::kColS + buf * KT;
-            if (!mbar_wait_bounded(&bars.s_full[buf], NS == 2 ? (j & 1) : ((j >> 1) & 1))) { ok = false; break; }
+            if (!bar_wait(&bars.s_full[buf], T::kTiles == 2 ? (j >> 1) & 1 : j & 1)) { ok = false; break; }
             tc_fence_after_sync();
             float x[KT];
             tmem_load_row(sa, x);
             if constexpr (CAP) {
+                // scores well inside the cap, as they mostly are, take a
+                // polynomial on the FMA pipe; two special functions else
+                float big = 0.0f;
 #pragma unroll
-                for (int i = 0; i < KT; ++i) x[i] = capped_log2<true>(x[i], cap);
+                for (int i = 0; i < KT; i += 2) big = max3(big, fabsf(x[i]), fabsf(x[i + 1]));
+                if (__all_sync(0xffffffffu, big <= in_reach)) {
+#pragma unroll
+                    for (int i = 0; i < KT; i += 2)
+                        apart(mul2(tanh_fma(mul2(two(x[i], x[i + 1]), two(cap_in, cap_in))), two(cap.out, cap.out)), x[i], x[i + 1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < KT; ++i) x[i] = capped_log2<true>(x[i], cap);
+                }
             } else if (a.scale < 0.0f) {
 #pragma unroll
                 for (int i = 0; i < KT; ++i) x[i] = -x[i];
@@ -431,24 +573,26 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                 for (int i = 0; i < KT; ++i)
                     if (i > hi || i < first) x[i] = -INFINITY;
             }
-            float mx[4] = {x[0], x[1], x[2], x[3]};
+            float mx[2] = {x[0], x[1]};
 #pragma unroll
-            for (int i = 4; i < KT; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
-            const float tile_max = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            // the reference maximum moves only when the weights would pass
-            // 2^8: the output tile in TMEM is rescaled in few of the steps
-            if (NS == 1 && j > 0) {
-                // two score tiles: these scores say nothing about the last
-                // product with V, whose output may be rescaled now and whose
-                // weights' barrier must have been passed
-                if (!mbar_wait_bounded(&bars.o_done[0], (j - 1) & 1)) { ok = false; break; }
-                tc_fence_after_sync();
+            for (int i = 2; i < KT - 2; i += 4) {
+                mx[0] = max3(mx[0], x[i], x[i + 1]);
+                mx[1] = max3(mx[1], x[i + 2], x[i + 3]);
             }
-            const bool grow = tile_max > m && (m == -INFINITY || (tile_max - m) * c > 8.0f);
+            const float tile_max = max3(max3(mx[0], x[KT - 2], x[KT - 1]), mx[1], mx[1]);
+            // The reference maximum moves only when weights would pass 2^8, so
+            // that the output in TMEM is rescaled in few of the steps.
+            // (a NaN becomes the maximum, and so the row's output)
+            const bool grow = !(tile_max <= m) && (m == -INFINITY || !((tile_max - m) * c <= 8.0f));
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = grow ? ex2((m - tile_max) * c) : 1.0f;  // m = -inf: 0
                 if (grow) m = tile_max, l *= f;
                 if (j > 0) {
+                    // (with one score tile, these scores followed that product)
+                    if (T::kTiles == 2) {
+                        if (!bar_wait(&bars.o_done[s], (j - 1) & 1)) { ok = false; break; }
+                        tc_fence_after_sync();
+                    }
 #pragma unroll 1
                     for (int k = 0; k < D; k += 32) {
                         float o[32];
@@ -460,26 +604,42 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                 }
             }
             const float base = m == -INFINITY ? 0.0f : m * c;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const f32x2 c2 = two(c, c), base2 = two(-base, -base);
+            f32x2 sum0 = two(0.0f, 0.0f), sum1 = sum0;
+            // with two score tiles, the barriers' phase of the tile before
+            // must have been passed before they are arrived at again
+            if (T::kTiles == 2 && j > 0 && !bar_wait(&bars.o_done[s], (j - 1) & 1)) { ok = false; break; }
 #pragma unroll
-            for (int k = 0; k < KT; k += 64) {
-                float w[32];
+            for (int half = 0; half < 2; ++half) {
+                constexpr int HW = KT / 4;  // words of half a tile's weights
+                float w[HW];
 #pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                    const float e0 = ex2(fmaf(x[k + i], c, -base)), e1 = ex2(fmaf(x[k + i + 1], c, -base));
-                    sum[i & 2] += e0, sum[(i & 2) + 1] += e1;
+                for (int i = 0; i < HW; ++i) {
+                    const int k = half * (KT / 2) + 2 * i;
+                    const f32x2 v = fma2(two(x[k], x[k + 1]), c2, base2);
+                    float e0, e1;
+                    if (i % 8 < T::kFmaOf8) {
+                        ex2_fma(v, e0, e1);
+                    } else {
+                        apart(v, e0, e1);
+                        e0 = ex2(e0), e1 = ex2(e1);
+                    }
+                    if (i & 1) sum1 = add2(sum1, two(e0, e1));
+                    else sum0 = add2(sum0, two(e0, e1));
                     const __nv_bfloat162 h = __floats2bfloat162_rn(e0, e1);
-                    w[i / 2] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&h));
+                    w[i] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&h));
                 }
-                tmem_store32(sa + k / 2, w);
+                tmem_store_row(sa + half * HW, w);
+                tmem_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(half ? &bars.p_ready[s] : &bars.p_half[s]);
             }
-            l += (sum[0] + sum[2]) + (sum[1] + sum[3]);
-            tmem_wait_st();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.p_ready[s]);
+            float sa0, sb0;
+            apart(add2(sum0, sum1), sa0, sb0);
+            l += sa0 + sb0;
         }
-        if (ok && mbar_wait_bounded(&bars.o_done[s], NS == 2 ? 0 : (n - 1) & 1)) {
+        if (ok && bar_wait(&bars.o_done[s], T::kTiles == 2 ? (n - 1) & 1 : 0)) {
             tc_fence_after_sync();
             const float f = 1.0f / l;
             __nv_bfloat16 *op = static_cast<__nv_bfloat16 *>(a.o) + ((size_t)(qt.base + qt.first + tok) * a.Hq + head) * D;
@@ -506,7 +666,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     __syncthreads();
     if (warp == T::kMmaWarp) {
         tc_fence_after_sync();
-        tmem_dealloc(tm, 512);
+        tmem_dealloc(tm, T::kCols);
     }
 }
 
