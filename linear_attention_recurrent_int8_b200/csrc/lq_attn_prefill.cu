@@ -307,7 +307,7 @@ struct Tc {
     static constexpr int kThreads = (kSoftWarps + 2) * 32;
     static constexpr int kSmem = 1024 + kStreams * kQBytes + kSlots * kSlotBytes;
     // of 8 pairs of weights, those exponentiated on the FMA pipe
-    static constexpr int kFmaOf8 = 2;
+    static constexpr int kFmaOf8 = 1;
     // TMEM columns: the score tiles, whose first half the weights overwrite,
     // then the outputs
     static constexpr uint32_t kColS = 0, kColO = 256;
@@ -573,13 +573,13 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                 for (int i = 0; i < KT; ++i)
                     if (i > hi || i < first) x[i] = -INFINITY;
             }
-            float mx[2] = {x[0], x[1]};
+            float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int i = 2; i < KT - 2; i += 4) {
-                mx[0] = max3(mx[0], x[i], x[i + 1]);
-                mx[1] = max3(mx[1], x[i + 2], x[i + 3]);
+            for (int i = 4; i < KT - 4; i += 8) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[i + 2 * e], x[i + 2 * e + 1]);
             }
-            const float tile_max = max3(max3(mx[0], x[KT - 2], x[KT - 1]), mx[1], mx[1]);
+            const float tile_max = max3(max3(mx[0], x[KT - 4], x[KT - 3]), max3(mx[1], x[KT - 2], x[KT - 1]), max3(mx[2], mx[3], mx[3]));
             // The reference maximum moves only when weights would pass 2^8, so
             // that the output in TMEM is rescaled in few of the steps.
             // (a NaN becomes the maximum, and so the row's output)
