@@ -19,7 +19,7 @@
 // parts (o, m, sum) in the workspace that a second launch joins in the order
 // of the line, so results do not depend on scheduling.
 //
-// BF16 (attn_tiles_bf16): query heads are the rows of a 16-row warp MMA.  The
+// BF16 (Bf16Core): query heads are the rows of a 16-row warp MMA.  The
 // softmax weights enter the product with V as two BF16 parts (p = hi + lo,
 // relative error 2^-17), so the output carries one rounding, its own.  With at
 // most 8 heads per key-value head the lower 8 rows hold hi, the upper 8 lo,
@@ -27,7 +27,8 @@
 // per token, a fifth of what the warp path can issue while DRAM delivers the
 // token, and accumulators in registers keep the warps independent.
 //
-// FP32 (attn_tiles_f32): FP32 FMAs, 8 query heads at a time.
+// FP32 (F32Core): the same with operands split into TF32 parts, 8 query heads
+// at a time.
 #include "lq_attn_common.cuh"
 
 namespace lq {
@@ -42,8 +43,8 @@ struct Tile {
     static constexpr int kBoxBytes = kTok * 128;
     static constexpr int kHalfBytes = kBoxes * kBoxBytes;       // K of a tile, then V
     static constexpr int kStageBytes = 2 * kHalfBytes;
-    // per-warp scratch of the FP32 path: 8 query rows, weights, factors
-    static constexpr int kScratch = BF16 ? 0 : 8 * D * 4 + kTok * 32 + 64;
+    // per-warp scratch: 8 query rows of FP32 (head size 256)
+    static constexpr int kScratch = BF16 || D < 256 ? 0 : 8 * (D + 4) * 4;
 };
 
 constexpr int kMaxStages = 8;
@@ -152,7 +153,7 @@ struct Bf16Core {
 
     // one tile: tokens tok0 .. tok0 + 15, visible lo .. len - 1
     __device__ __forceinline__ void tile(const AttnArgs &a, unsigned char *st, int tok0, int lo, int len, int lane,
-                                         unsigned char *) {
+                                         unsigned char *, int, int, int) {
         using T = Tile<D, true>;
         const int mi = lane >> 3, ri = lane & 7, t = lane & 3;
         const uint32_t kb = smem_u32(st), vb = kb + T::kHalfBytes;
@@ -289,175 +290,208 @@ struct Bf16Core {
     }
 };
 
-// The same over tiles of FP32 rows, 8 query rows.
+// The same over tiles of FP32 rows, 8 query rows.  Every FP32 operand enters
+// the TF32 MMAs as two parts, x = hi + lo with hi its upper 11 bits: the upper
+// 8 rows of the A operand hold the hi parts and the lower 8 the lo parts of
+// the 8 query rows (or of their weights), and B comes once as hi and once as
+// lo, so two MMAs give all four products (what is lost of lo is 2^-22 of x).
 template <int D>
 struct F32Core {
     using T = Tile<D, false>;
-    static constexpr int TOK = T::kTok;
-    static constexpr int NP = 32 / TOK;             // lanes of one token in q . k
-    static constexpr int NRL = 8 / NP;              // rows a lane holds after the reduction
-    static constexpr int LPR = D / 4 < 32 ? D / 4 : 32;  // lanes across a row of V
-    static constexpr int TG = 32 / LPR;             // token groups in p V
-    static constexpr int NV = D / (4 * LPR);        // float4 of a row per lane
-    float o[8][4 * NV], m[NRL], l[NRL];
+    static constexpr int TOK = T::kTok, NT = TOK / 8, NB = T::kBoxes;
+    static constexpr bool kKeepQ = D < 256;  // split query rows in registers, else FP32 rows in scratch
+    static constexpr int kLd = D + 4;        // scratch row stride: rows on distinct banks
+    float q[kKeepQ ? NB : 1][2][8];
+    float o[NB][4][4], m, l;
 
-    __device__ __forceinline__ static float *q_smem(unsigned char *sc) { return reinterpret_cast<float *>(sc); }
-    __device__ __forceinline__ static float *p_smem(unsigned char *sc) { return reinterpret_cast<float *>(sc) + 8 * D; }
-    __device__ __forceinline__ static float *f_smem(unsigned char *sc) { return reinterpret_cast<float *>(sc) + 8 * D + 8 * TOK; }
-
-    // the first of the rows a lane holds after the reduction
-    __device__ __forceinline__ static int row0(int lane) {
-        const int part = lane / TOK;
-        return NP == 4 ? 4 * (part >> 1) + 2 * (part & 1) : 4 * part;
+    __device__ __forceinline__ static void split(float x, float &hi, float &lo) {
+        hi = __uint_as_float(__float_as_uint(x) & 0xFFFFE000u);
+        lo = x - hi;
+    }
+    __device__ __forceinline__ static void split4(const float4 &x, float (&v)[8]) {
+        split(x.x, v[0], v[1]), split(x.y, v[2], v[3]), split(x.z, v[4], v[5]), split(x.w, v[6], v[7]);
+    }
+    __device__ __forceinline__ static void mma(float (&d)[4], const float *a, float b0, float b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])),
+              "r"(__float_as_uint(a[3])), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
     }
 
+    // Channels of a box are dealt to the MMA's K so that a lane reads 16 bytes
+    // at a time: lane t holds chunks 2t and 2t + 1 (of 4 channels) of its row.
     __device__ __forceinline__ void begin(const AttnArgs &a, int b, int head0, int rows, int lane, unsigned char *sc) {
-        const float4 *qp = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + ((size_t)b * a.Hq + head0) * D);
-        __syncwarp();
-        for (int i = lane; i < 8 * D / 4; i += 32)
-            reinterpret_cast<float4 *>(q_smem(sc))[i] = i < rows * (D / 4) ? __ldg(qp + i) : make_float4(0, 0, 0, 0);
-        __syncwarp();
+        const int g = lane >> 2, t = lane & 3;
+        const float *qp = static_cast<const float *>(a.q) + ((size_t)b * a.Hq + head0) * D;
+        const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if constexpr (kKeepQ) {
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
+            for (int x = 0; x < NB; ++x)
 #pragma unroll
-            for (int e = 0; e < 4 * NV; ++e) o[r][e] = 0.0f;
+                for (int j = 0; j < 2; ++j)
+                    split4(g < rows ? __ldg(reinterpret_cast<const float4 *>(qp + g * D + 32 * x + 4 * (2 * t + j))) : zero, q[x][j]);
+        } else {
+            __syncwarp();
+            for (int i = lane; i < 8 * (D / 4); i += 32) {
+                const int r = i / (D / 4), c = 4 * (i % (D / 4));
+                *reinterpret_cast<float4 *>(reinterpret_cast<float *>(sc) + r * kLd + c) =
+                    r < rows ? __ldg(reinterpret_cast<const float4 *>(qp + r * D + c)) : zero;
+            }
+            __syncwarp();
+        }
 #pragma unroll
-        for (int r = 0; r < NRL; ++r) m[r] = -INFINITY, l[r] = 0.0f;
+        for (int x = 0; x < NB; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[x][i][e] = 0.0f;
+        m = -INFINITY, l = 0.0f;
     }
 
     __device__ __forceinline__ void tile(const AttnArgs &a, unsigned char *st, int tok0, int lo, int len, int lane,
-                                         unsigned char *sc) {
-        const int tok = lane % TOK, part = lane / TOK;
-        float s[8];
+                                         unsigned char *sc, int b, int head0, int rows) {
+        const int g = lane >> 2, t = lane & 3;
+        float s[NT][2];  // scores of tokens 8 n + 2 t, 8 n + 2 t + 1 with row g
+        {
+            float c[NT][4];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) s[r] = 0.0f;
-        // a lane takes 1 / NP of its token's channels; the parts start at
-        // different 16-byte chunks so that their q reads hit distinct banks
-        constexpr int BPP = T::kBoxes / NP;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int bx = 0; bx < BPP; ++bx) {
-            const int box = part * BPP + bx;
-            const unsigned char *kr = st + box * T::kBoxBytes + tok * 128;
-            const float *qr = q_smem(sc) + box * 32;
-#pragma unroll 2
-            for (int c0 = 0; c0 < 8; ++c0) {
-                const int c = (c0 + part * (8 / NP)) & 7;
-                const float4 k = *reinterpret_cast<const float4 *>(kr + ((c ^ (tok & 7)) << 4));
+                for (int e = 0; e < 4; ++e) c[n][e] = 0.0f;
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const float4 q = *reinterpret_cast<const float4 *>(qr + r * D + 4 * c);
-                    s[r] = fmaf(q.x, k.x, s[r]);
-                    s[r] = fmaf(q.y, k.y, s[r]);
-                    s[r] = fmaf(q.z, k.z, s[r]);
-                    s[r] = fmaf(q.w, k.w, s[r]);
+            for (int x = 0; x < NB; ++x)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float qv[8];
+                    if constexpr (kKeepQ) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) qv[e] = q[x][j][e];
+                    } else {
+                        split4(*reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sc) + g * kLd + 32 * x + 4 * (2 * t + j)), qv);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float k[8];
+                        split4(*reinterpret_cast<const float4 *>(st + x * T::kBoxBytes + (8 * n + g) * 128 + (((2 * t + j) ^ g) << 4)), k);
+                        mma(c[n], qv, k[0], k[2]);
+                        mma(c[n], qv, k[1], k[3]);
+                        mma(c[n], qv + 4, k[4], k[6]);
+                        mma(c[n], qv + 4, k[5], k[7]);
+                    }
                 }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[n][0] = c[n][0] + c[n][2], s[n][1] = c[n][1] + c[n][3];
+        }
+        const bool part = tok0 + TOK > len || tok0 < lo;
+        bool seen[NT][2], odd = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int tok = tok0 + 8 * n + 2 * t + e;
+                seen[n][e] = !part || (tok >= lo && tok < len);
+                odd = odd || (seen[n][e] && s[n][e] != s[n][e]);
             }
-        }
-        // sums over the parts: halving exchanges leave rows row0 .. row0 + NRL - 1 here
+        if (__any_sync(0xffffffffu, odd)) {
+            // The split turns an infinity into NaN: such a tile's scores are
+            // formed again, in FP32.
+            const float *qp = static_cast<const float *>(a.q) + ((size_t)b * a.Hq + head0 + g) * D;
+#pragma unroll 1
+            for (int i = 0; i < 2 * NT && g < rows; ++i) {
+                const int r = 8 * (i >> 1) + 2 * t + (i & 1);
+                float x = 0.0f;
+#pragma unroll 1
+                for (int d = 0; d < D; ++d)
+                    x = fmaf(__ldg(qp + d), *reinterpret_cast<const float *>(st + (d >> 5) * T::kBoxBytes + r * 128 +
+                                                                             ((((d >> 2) & 7) ^ (r & 7)) << 4) + 4 * (d & 3)), x);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const bool up = (lane & 16) != 0;
-            const float send = up ? s[r] : s[r + 4];
-            s[r] = (up ? s[r + 4] : s[r]) + __shfl_xor_sync(0xffffffffu, send, 16);
-        }
-        if constexpr (NP == 4) {
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const bool up = (lane & 8) != 0;
-                const float send = up ? s[r] : s[r + 2];
-                s[r] = (up ? s[r + 2] : s[r]) + __shfl_xor_sync(0xffffffffu, send, 8);
-            }
-        }
-        const bool seen = tok0 + tok >= lo && tok0 + tok < len;
-        const SoftCap cap = soft_cap<false>(a.scale, a.softcap);
-        bool grew = false;
-        float mx[NRL];
-#pragma unroll
-        for (int r = 0; r < NRL; ++r) {
-            s[r] = a.softcap > 0.0f ? capped_log2<false>(s[r], cap) : s[r] * (a.scale * kLog2e);
-            if (!seen) s[r] = -INFINITY;
-            mx[r] = group_max<TOK>(s[r]);
-            grew = grew || mx[r] > m[r];
-        }
-        const int r0 = row0(lane);
-        if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-            for (int r = 0; r < NRL; ++r) {
-                const float n = fmaxf(m[r], mx[r]);
-                const float f = n == -INFINITY ? 1.0f : ex2(m[r] - n);
-                m[r] = n;
-                l[r] *= f;
-                if (tok == 0) f_smem(sc)[r0 + r] = f;
+                    for (int e = 0; e < 2; ++e)
+                        if (2 * n + e == i) s[n][e] = x;
             }
             __syncwarp();
+        }
+        const SoftCap cap = soft_cap<false>(a.scale, a.softcap);
+        float mx = -INFINITY;
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const float f = f_smem(sc)[r];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4 * NV; ++e) o[r][e] *= f;
+            for (int e = 0; e < 2; ++e) {
+                s[n][e] = a.softcap > 0.0f ? capped_log2<false>(s[n][e], cap) : s[n][e] * (a.scale * kLog2e);
+                if (!seen[n][e]) s[n][e] = -INFINITY;
+                mx = fmaxf(mx, s[n][e]);
             }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        if (__any_sync(0xffffffffu, mx > m)) {
+            const float n = fmaxf(m, mx), f = n == -INFINITY ? 1.0f : ex2(m - n);
+            m = n;
+            l *= f;
+#pragma unroll
+            for (int x = 0; x < NB; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[x][i][e] *= f;
         }
+        const float base = m == -INFINITY ? 0.0f : m;
+        float p[NT][4];
 #pragma unroll
-        for (int r = 0; r < NRL; ++r) {
-            const float p = ex2(s[r] - (m[r] == -INFINITY ? 0.0f : m[r]));
-            l[r] += p;
-            p_smem(sc)[8 * tok + r0 + r] = p;
+        for (int n = 0; n < NT; ++n) {
+            const float p0 = ex2(s[n][0] - base), p1 = ex2(s[n][1] - base);
+            l += p0 + p1;
+            split(p0, p[n][0], p[n][1]);
+            split(p1, p[n][2], p[n][3]);
         }
-        __syncwarp();
-        // only visible tokens: the others' values may be NaN
-        const int t_lo = lo > tok0 ? lo - tok0 : 0, t_hi = len - tok0 < TOK ? len - tok0 : TOK;
-        const int vl = lane % LPR, tg = lane / LPR;
-#pragma unroll 4
-        for (int t = t_lo + tg; t < t_hi; t += TG) {
-            const float4 pa = *reinterpret_cast<const float4 *>(p_smem(sc) + 8 * t);
-            const float4 pb = *reinterpret_cast<const float4 *>(p_smem(sc) + 8 * t + 4);
-            const float p[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+        if (part) {
+            // rows of V that are not visible may hold NaN: weight 0 would not silence them
+            for (int r = 0; r < TOK; ++r) {
+                if (tok0 + r >= lo && tok0 + r < len) continue;
+                for (int ch = lane; ch < D / 4; ch += 32)
+                    *reinterpret_cast<uint4 *>(st + T::kHalfBytes + (ch >> 3) * T::kBoxBytes + r * 128 + (ch & 7) * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();  // before the stage's next TMA write
+            __syncwarp();
+        }
+        // lane (g, t) reads chunk g of the rows of its two tokens: channel
+        // 4 g + i of a box is column g of the box's MMA i
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int ch = vl + 32 * i;  // 16-byte chunk of the row
-                const float4 v = *reinterpret_cast<const float4 *>(st + T::kHalfBytes + (ch >> 3) * T::kBoxBytes + t * 128 +
-                                                                  (((ch & 7) ^ (t & 7)) << 4));
+        for (int x = 0; x < NB; ++x)
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    o[r][4 * i] = fmaf(p[r], v.x, o[r][4 * i]);
-                    o[r][4 * i + 1] = fmaf(p[r], v.y, o[r][4 * i + 1]);
-                    o[r][4 * i + 2] = fmaf(p[r], v.z, o[r][4 * i + 2]);
-                    o[r][4 * i + 3] = fmaf(p[r], v.w, o[r][4 * i + 3]);
+            for (int n = 0; n < NT; ++n) {
+                const unsigned char *vp = st + T::kHalfBytes + x * T::kBoxBytes + (8 * n + 2 * t) * 128;
+                float v0[8], v1[8];
+                split4(*reinterpret_cast<const float4 *>(vp + ((g ^ (2 * t)) << 4)), v0);
+                split4(*reinterpret_cast<const float4 *>(vp + 128 + ((g ^ (2 * t + 1)) << 4)), v1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mma(o[x][i], p[n], v0[2 * i], v1[2 * i]);
+                    mma(o[x][i], p[n], v0[2 * i + 1], v1[2 * i + 1]);
                 }
             }
-        }
     }
 
     __device__ __forceinline__ void end(const AttnArgs &a, int b, int head0, int rows, float *part, int lane,
-                                        unsigned char *sc) {
-        const int tok = lane % TOK, r0 = row0(lane), vl = lane % LPR;
-        __syncwarp();
+                                        unsigned char *) {
+        const int g = lane >> 2, t = lane & 3;
+        float sum = l;
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (g >= rows) return;
+        const float f = part ? 1.0f : 1.0f / sum;
+        float *dst = part ? part + g * D : static_cast<float *>(a.o) + ((size_t)b * a.Hq + head0 + g) * D;
 #pragma unroll
-        for (int r = 0; r < NRL; ++r) {
-            const float sum = group_sum<TOK>(l[r]);
-            if (tok == 0) {
-                f_smem(sc)[r0 + r] = sum;
-                if (part && r0 + r < rows)
-                    *reinterpret_cast<float2 *>(part + 8 * D + 2 * (r0 + r)) = make_float2(m[r], sum);
-            }
-        }
-        __syncwarp();
+        for (int x = 0; x < NB; ++x)
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            if constexpr (TG == 2) {
-#pragma unroll
-                for (int e = 0; e < 4 * NV; ++e) o[r][e] += __shfl_xor_sync(0xffffffffu, o[r][e], 16);
-            }
-            if (r < rows && lane < LPR) {
-                const float f = part ? 1.0f : 1.0f / f_smem(sc)[r];
-                float *dst = part ? part + r * D : static_cast<float *>(a.o) + ((size_t)b * a.Hq + head0 + r) * D;
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    *reinterpret_cast<float4 *>(dst + 4 * (vl + 32 * i)) =
-                        make_float4(o[r][4 * i] * f, o[r][4 * i + 1] * f, o[r][4 * i + 2] * f, o[r][4 * i + 3] * f);
-            }
-        }
-        __syncwarp();
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<float4 *>(dst + 32 * x + 8 * t + 4 * e) =
+                    make_float4((o[x][0][e] + o[x][0][e + 2]) * f, (o[x][1][e] + o[x][1][e + 2]) * f,
+                                (o[x][2][e] + o[x][2][e + 2]) * f, (o[x][3][e] + o[x][3][e + 2]) * f);
+        if (part && t == 0) *reinterpret_cast<float2 *>(part + 8 * D + 2 * g) = make_float2(m, sum);
     }
 };
 
@@ -589,7 +623,7 @@ __global__ void __launch_bounds__(Tile<D, BF16>::kWarps * 32, 1)
             return;
         }
         unsigned char *stage = my_ring + st * T::kStageBytes;
-        core.tile(a, stage, (c.t0 + c.t) * TOK, c.lo, c.len, lane, sc);
+        core.tile(a, stage, (c.t0 + c.t) * TOK, c.lo, c.len, lane, sc, c.b, head0, rows);
         __syncwarp();
         if (filled < run) issue();
         if (++st == pl.stages) st = 0, ph ^= 1;
