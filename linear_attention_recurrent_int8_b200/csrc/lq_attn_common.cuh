@@ -73,6 +73,27 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// FP32 operands of TF32 MMAs in two parts: x = hi + lo, hi the upper 11 bits
+// (what the MMA drops of lo is 2^-22 of x).  An infinity becomes (inf, NaN).
+__device__ __forceinline__ void split_tf32(float x, float &hi, float &lo) {
+    hi = __uint_as_float(__float_as_uint(x) & 0xFFFFE000u);
+    lo = x - hi;
+}
+// (hi, lo) of four values.
+__device__ __forceinline__ void split_tf32(const float4 &x, float (&v)[8]) {
+    split_tf32(x.x, v[0], v[1]), split_tf32(x.y, v[2], v[3]), split_tf32(x.z, v[4], v[5]), split_tf32(x.w, v[6], v[7]);
+}
+
+// D += A B, 16 x 8 x 8, TF32 operands, FP32 sums.
+__device__ __forceinline__ void mma_1688(float (&d)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
+          "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -294,30 +294,18 @@ struct Bf16Core {
 // the TF32 MMAs as two parts, x = hi + lo with hi its upper 11 bits: the upper
 // 8 rows of the A operand hold the hi parts and the lower 8 the lo parts of
 // the 8 query rows (or of their weights), and B comes once as hi and once as
-// lo, so two MMAs give all four products (what is lost of lo is 2^-22 of x).
+// lo, so two MMAs give all four products.  A row of scratch (head size 256) is
+// D + 4 floats long, which puts the rows on distinct banks.
 template <int D>
 struct F32Core {
     using T = Tile<D, false>;
     static constexpr int TOK = T::kTok, NT = TOK / 8, NB = T::kBoxes;
     static constexpr bool kKeepQ = D < 256;  // split query rows in registers, else FP32 rows in scratch
-    static constexpr int kLd = D + 4;        // scratch row stride: rows on distinct banks
     float q[kKeepQ ? NB : 1][2][8];
     float o[NB][4][4], m, l;
 
-    __device__ __forceinline__ static void split(float x, float &hi, float &lo) {
-        hi = __uint_as_float(__float_as_uint(x) & 0xFFFFE000u);
-        lo = x - hi;
-    }
-    __device__ __forceinline__ static void split4(const float4 &x, float (&v)[8]) {
-        split(x.x, v[0], v[1]), split(x.y, v[2], v[3]), split(x.z, v[4], v[5]), split(x.w, v[6], v[7]);
-    }
     __device__ __forceinline__ static void mma(float (&d)[4], const float *a, float b0, float b1) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-            "{%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])),
-              "r"(__float_as_uint(a[3])), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+        mma_1688(d, a[0], a[1], a[2], a[3], b0, b1);
     }
 
     // Channels of a box are dealt to the MMA's K so that a lane reads 16 bytes
@@ -331,12 +319,12 @@ struct F32Core {
             for (int x = 0; x < NB; ++x)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    split4(g < rows ? __ldg(reinterpret_cast<const float4 *>(qp + g * D + 32 * x + 4 * (2 * t + j))) : zero, q[x][j]);
+                    split_tf32(g < rows ? __ldg(reinterpret_cast<const float4 *>(qp + g * D + 32 * x + 4 * (2 * t + j))) : zero, q[x][j]);
         } else {
             __syncwarp();
             for (int i = lane; i < 8 * (D / 4); i += 32) {
                 const int r = i / (D / 4), c = 4 * (i % (D / 4));
-                *reinterpret_cast<float4 *>(reinterpret_cast<float *>(sc) + r * kLd + c) =
+                *reinterpret_cast<float4 *>(reinterpret_cast<float *>(sc) + r * (D + 4) + c) =
                     r < rows ? __ldg(reinterpret_cast<const float4 *>(qp + r * D + c)) : zero;
             }
             __syncwarp();
@@ -369,12 +357,12 @@ struct F32Core {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) qv[e] = q[x][j][e];
                     } else {
-                        split4(*reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sc) + g * kLd + 32 * x + 4 * (2 * t + j)), qv);
+                        split_tf32(*reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sc) + g * (D + 4) + 32 * x + 4 * (2 * t + j)), qv);
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float k[8];
-                        split4(*reinterpret_cast<const float4 *>(st + x * T::kBoxBytes + (8 * n + g) * 128 + (((2 * t + j) ^ g) << 4)), k);
+                        split_tf32(*reinterpret_cast<const float4 *>(st + x * T::kBoxBytes + (8 * n + g) * 128 + (((2 * t + j) ^ g) << 4)), k);
                         mma(c[n], qv, k[0], k[2]);
                         mma(c[n], qv, k[1], k[3]);
                         mma(c[n], qv + 4, k[4], k[6]);
@@ -443,8 +431,8 @@ struct F32Core {
         for (int n = 0; n < NT; ++n) {
             const float p0 = ex2(s[n][0] - base), p1 = ex2(s[n][1] - base);
             l += p0 + p1;
-            split(p0, p[n][0], p[n][1]);
-            split(p1, p[n][2], p[n][3]);
+            split_tf32(p0, p[n][0], p[n][1]);
+            split_tf32(p1, p[n][2], p[n][3]);
         }
         if (part) {
             // rows of V that are not visible may hold NaN: weight 0 would not silence them
@@ -465,8 +453,8 @@ struct F32Core {
             for (int n = 0; n < NT; ++n) {
                 const unsigned char *vp = st + T::kHalfBytes + x * T::kBoxBytes + (8 * n + 2 * t) * 128;
                 float v0[8], v1[8];
-                split4(*reinterpret_cast<const float4 *>(vp + ((g ^ (2 * t)) << 4)), v0);
-                split4(*reinterpret_cast<const float4 *>(vp + 128 + ((g ^ (2 * t + 1)) << 4)), v1);
+                split_tf32(*reinterpret_cast<const float4 *>(vp + ((g ^ (2 * t)) << 4)), v0);
+                split_tf32(*reinterpret_cast<const float4 *>(vp + 128 + ((g ^ (2 * t + 1)) << 4)), v1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     mma(o[x][i], p[n], v0[2 * i], v1[2 * i]);

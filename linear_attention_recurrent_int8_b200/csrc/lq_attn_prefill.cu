@@ -1,169 +1,305 @@
 // lq_attn_prefill.cu -- attention of runs of new tokens over the paged
 // key-value cache (lq_attn_prefill), causal from each token's own position.
 //
-// attn_prefill_simt: 64 query rows of one head per block, key tiles staged in
-// shared memory as FP32, 4 x 4 register tiles of FP32 FMAs, running maximum
-// and sum per row.
+// attn_prefill_tc (BF16) runs on tcgen05 with scores, weights and outputs in
+// TMEM; attn_prefill_f32 on warp MMAs with TF32 operands in two parts.  Both
+// pack the query heads that share a key-value head into the rows of a tile
+// (head fastest), so that a tile spans few tokens: its causal edge is short
+// and its keys are read once for all of its heads.
 #include "lq_attn_common.cuh"
 #include "lq_tc.cuh"
 
 namespace lq {
 namespace {
 
+// ---------------------------------------------------------------------------
+// FP32: warp MMAs on operands in two TF32 parts
+// ---------------------------------------------------------------------------
+
 template <int D>
-struct Simt {
-    static constexpr int kRows = 64, kThreads = 256;
-    static constexpr int kKeys = D == 256 ? 32 : 64;
-    static constexpr int kCols = kKeys / 16;     // key columns of a thread
-    static constexpr int kLd = D + 4;            // row stride of Q and K: rows on distinct banks
-    static constexpr int kSmem = (kRows * kLd + kKeys * kLd + kKeys * D + kRows * (kKeys + 4)) * 4;
+struct F32 {
+    static constexpr int kRows = 32, kThreads = 128;
+    static constexpr int kKeys = D == 64 ? 32 : 16;         // keys of a tile
+    static constexpr int kBoxes = D / 32;                   // 128-byte column blocks
+    static constexpr int kBoxBytes = kKeys * 128;
+    static constexpr int kHalfBytes = kBoxes * kBoxBytes;   // K of a tile, then V
+    static constexpr int kStageBytes = 2 * kHalfBytes;
+    static constexpr int kLd = D + 4;                       // row stride of Q: rows on distinct banks
+    static constexpr int kSmem = 1024 + 4 * kStageBytes + kRows * kLd * 4;
 };
 
-__device__ __forceinline__ float4 load4(const void *p, size_t i) {
-    return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-}
-
+// One block: 32 rows, each a (token, head) pair of heads that share a
+// key-value head (head fastest).  Warp w takes 16 rows (w % 2) and every
+// second tile of keys (w / 2); the two warps of a tile share its two-stage
+// ring, and the two halves of a row's keys are joined at the end.  Products
+// of two-part operands: hi hi + hi lo + lo hi, 3 MMAs.
 template <int D>
-__global__ void __launch_bounds__(256) attn_prefill_simt(const AttnArgs a) {
-    using S = Simt<D>;
-    constexpr int LD = S::kLd, KT = S::kKeys, NC = S::kCols, PL = KT + 4;
-    extern __shared__ __align__(16) float sm[];
-    float *qs = sm, *ks = qs + S::kRows * LD, *vs = ks + KT * LD, *ps = vs + KT * D;
-    __shared__ int find[S::kThreads / 32 + 6];
+__global__ void __launch_bounds__(F32<D>::kThreads) attn_prefill_f32(const __grid_constant__ CUtensorMap kmap,
+                                                                     const __grid_constant__ CUtensorMap vmap,
+                                                                     const AttnArgs a, const int group_shift) {
+    using T = F32<D>;
+    constexpr int KT = T::kKeys, NB = T::kBoxes, NT = KT / 8, LD = T::kLd;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float *qs = reinterpret_cast<float *>(ring + 4 * T::kStageBytes);
+    __shared__ uint64_t full[2][2], empty[2][2];
+    __shared__ int find[T::kThreads / 32 + 6];
     // the last tiles see the most keys: they go first
-    const QueryTile qt = find_query_tile<S::kThreads>(a, S::kRows, gridDim.x - 1 - (long long)blockIdx.x, find);
+    const QueryTile qt = find_query_tile<T::kThreads>(a, T::kRows >> group_shift, gridDim.x - 1 - (long long)blockIdx.x, find);
     if (qt.rows <= 0) return;
-    const int tid = threadIdx.x, rg = tid >> 4, cg = tid & 15;
-    const int h = blockIdx.y, kv = h / (a.Hq / a.Hkv);
-    for (int i = tid; i < S::kRows * (D / 4); i += S::kThreads) {
-        const int r = i / (D / 4), c = 4 * (i % (D / 4));
-        float4 x = make_float4(0, 0, 0, 0);
-        if (r < qt.rows) x = load4(a.q, ((size_t)(qt.base + qt.first + r) * a.Hq + h) * D + c);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int rg = warp & 1, kg = warp >> 1;
+    const int heads = 1 << group_shift, h0 = blockIdx.y << group_shift, kv = h0 / (a.Hq / a.Hkv);
+    const int p0 = qt.start + qt.first, len = p0 + qt.rows;  // keys any row sees: lo .. len - 1
+    const int lo = a.window > 0 && p0 + 1 > a.window ? p0 + 1 - a.window : 0;
+    const int k_first = lo / KT, n = (len - 1) / KT - k_first + 1;
+
+    if (tid < 4) mbar_init(&full[tid >> 1][tid & 1], 1), mbar_init(&empty[tid >> 1][tid & 1], 2);
+    __syncthreads();
+    // one lane of a key group fills its ring
+    auto issue = [&](int i) {  // the group's i-th tile
+        const int st = i & 1, k0 = (k_first + 2 * i + kg) * KT;
+        uint64_t *bar = &full[kg][st];
+        unsigned char *dst = ring + (2 * kg + st) * T::kStageBytes;
+        mbar_arrive_expect_tx(bar, T::kStageBytes);
+        for (int r = 0; r < KT; r += 16) {
+            const int tok = k0 + r;
+            int z = -1;  // rows past the visible keys are filled with zeros
+            if (tok < len && tok + 16 > lo) {
+                const int page = __ldg(a.block_table + (size_t)qt.b * a.max_pages + (tok >> a.page_shift));
+                if (page >= 0 && page < a.num_pages) z = page * a.Hkv + kv;
+                else atomicOr(&g_dev_error, kErrBadPage);
+            }
+            for (int x = 0; x < NB; ++x) {
+                tma_page_load(dst + x * T::kBoxBytes + r * 128, &kmap, 32 * x, tok & (a.page_size - 1), z, bar);
+                tma_page_load(dst + T::kHalfBytes + x * T::kBoxBytes + r * 128, &vmap, 32 * x, tok & (a.page_size - 1), z, bar);
+            }
+        }
+    };
+    const int mine = kg < n ? (n - kg + 1) / 2 : 0;  // tiles of the group
+    const bool producer = rg == 0 && lane == 0;
+    if (producer && mine > 0) issue(0);
+    for (int i = tid; i < T::kRows * (D / 4); i += T::kThreads) {
+        const int r = i / (D / 4), c = 4 * (i % (D / 4)), tok = r >> group_shift;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (tok < qt.rows)
+            x = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) +
+                                                  ((size_t)(qt.base + qt.first + tok) * a.Hq + h0 + (r & (heads - 1))) * D + c);
         *reinterpret_cast<float4 *>(qs + r * LD + c) = x;
     }
-    const int p0 = qt.start + qt.first;               // position of row 0
-    const int len = p0 + qt.rows;                     // keys any row sees: [lo, len)
-    const int lo = a.window > 0 && p0 + 1 > a.window ? p0 + 1 - a.window : 0;
+    __syncthreads();
+
     const SoftCap cap = soft_cap<false>(a.scale, a.softcap);
-    float o[4][D / 16], m[4], l[4];
+    int pos[2];  // of rows g and g + 8
+    for (int r = 0; r < 2; ++r) pos[r] = p0 + ((16 * rg + g + 8 * r) >> group_shift);
+    const int pw0 = p0 + ((16 * rg) >> group_shift), pw1 = p0 + ((16 * rg + 15) >> group_shift);
+    const float *qr = qs + (16 * rg + g) * LD;
+    float o[NB][4][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        m[r] = -INFINITY, l[r] = 0.0f;
+    for (int x = 0; x < NB; ++x)
 #pragma unroll
-        for (int e = 0; e < D / 16; ++e) o[r][e] = 0.0f;
-    }
-    for (int k0 = lo / KT * KT; k0 < len; k0 += KT) {
-        __syncthreads();
-        for (int i = tid; i < KT * (D / 4); i += S::kThreads) {
-            const int r = i / (D / 4), c = 4 * (i % (D / 4)), tok = k0 + r;
-            float4 kx = make_float4(0, 0, 0, 0), vx = kx;
-            if (tok >= lo && tok < len) {
-                const int page = __ldg(a.block_table + (size_t)qt.b * a.max_pages + (tok >> a.page_shift));
-                if (page >= 0 && page < a.num_pages) {
-                    const size_t at = (((size_t)page * a.Hkv + kv) * a.page_size + (tok & (a.page_size - 1))) * D + c;
-                    kx = load4(a.k_pages, at);
-                    vx = load4(a.v_pages, at);
-                } else if (c == 0) {
-                    atomicOr(&g_dev_error, kErrBadPage);
-                }
-            }
-            *reinterpret_cast<float4 *>(ks + r * LD + c) = kx;
-            *reinterpret_cast<float4 *>(vs + r * D + c) = vx;
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[x][i][e] = 0.0f;
+    bool ok = true;
+    for (int it = 0; it < mine; ++it) {
+        const int st = it & 1, k0 = (k_first + 2 * it + kg) * KT;
+        unsigned char *stage = ring + (2 * kg + st) * T::kStageBytes;
+        if (it + 1 < mine && producer) {
+            // the other stage, once both warps have left its last tile
+            if (it > 0) ok = bar_wait(&empty[kg][st ^ 1], ((it - 1) >> 1) & 1);
+            if (ok) issue(it + 1);
         }
-        __syncthreads();
-        float s[4][NC];
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok && bar_wait(&full[kg][st], (it >> 1) & 1));
+        if (!ok) break;
+        float s[NT][4];  // rows g, g (tokens 2t, 2t + 1), g + 8, g + 8
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int k = 0; k < NT; ++k)
 #pragma unroll
-            for (int j = 0; j < NC; ++j) s[r][j] = 0.0f;
-#pragma unroll 4
-        for (int c = 0; c < D; c += 4) {
-            float4 qv[4], kx[NC];
+            for (int e = 0; e < 4; ++e) s[k][e] = 0.0f;
+        // a lane reads 16 bytes of channels at a time: lane t takes chunks 2t
+        // and 2t + 1 of a box as two K steps
 #pragma unroll
-            for (int r = 0; r < 4; ++r) qv[r] = *reinterpret_cast<const float4 *>(qs + (4 * rg + r) * LD + c);
+        for (int x = 0; x < NB; ++x)
 #pragma unroll
-            for (int j = 0; j < NC; ++j) kx[j] = *reinterpret_cast<const float4 *>(ks + (cg + 16 * j) * LD + c);
+            for (int j = 0; j < 2; ++j) {
+                float qa[8], qb[8];
+                split_tf32(*reinterpret_cast<const float4 *>(qr + 32 * x + 4 * (2 * t + j)), qa);
+                split_tf32(*reinterpret_cast<const float4 *>(qr + 8 * LD + 32 * x + 4 * (2 * t + j)), qb);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+                for (int k = 0; k < NT; ++k) {
+                    float kk[8];
+                    split_tf32(*reinterpret_cast<const float4 *>(stage + x * T::kBoxBytes + (8 * k + g) * 128 + (((2 * t + j) ^ g) << 4)), kk);
 #pragma unroll
-                for (int j = 0; j < NC; ++j) {
-                    s[r][j] = fmaf(qv[r].x, kx[j].x, s[r][j]);
-                    s[r][j] = fmaf(qv[r].y, kx[j].y, s[r][j]);
-                    s[r][j] = fmaf(qv[r].z, kx[j].z, s[r][j]);
-                    s[r][j] = fmaf(qv[r].w, kx[j].w, s[r][j]);
-                }
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int p = p0 + 4 * rg + r;
-            float mx = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < NC; ++j) {
-                const int tok = k0 + cg + 16 * j;
-                const bool seen = tok <= p && (a.window == 0 || tok > p - a.window);
-                float x = a.softcap > 0.0f ? capped_log2<false>(s[r][j], cap) : s[r][j] * (a.scale * kLog2e);
-                s[r][j] = seen ? x : -INFINITY;
-                mx = fmaxf(mx, s[r][j]);
-            }
-            mx = group_max<16>(mx);
-            const float n = fmaxf(m[r], mx);
-            const float base = n == -INFINITY ? 0.0f : n;
-            const float f = ex2(m[r] - base);
-            m[r] = n;
-            l[r] *= f;
-#pragma unroll
-            for (int e = 0; e < D / 16; ++e) o[r][e] *= f;
-#pragma unroll
-            for (int j = 0; j < NC; ++j) {
-                const float w = ex2(s[r][j] - base);
-                l[r] += w;
-                ps[(4 * rg + r) * PL + cg + 16 * j] = w;
-            }
-        }
-        __syncwarp();  // the rows of P are read by the half-warp that wrote them
-#pragma unroll 2
-        for (int k = 0; k < KT; k += 4) {
-            float4 pv[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) pv[r] = *reinterpret_cast<const float4 *>(ps + (4 * rg + r) * PL + k);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-                for (int e = 0; e < D / 64; ++e) {
-                    const float4 v = *reinterpret_cast<const float4 *>(vs + (k + kk) * D + 64 * e + 4 * cg);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float w = kk == 0 ? pv[r].x : kk == 1 ? pv[r].y : kk == 2 ? pv[r].z : pv[r].w;
-                        o[r][4 * e] = fmaf(w, v.x, o[r][4 * e]);
-                        o[r][4 * e + 1] = fmaf(w, v.y, o[r][4 * e + 1]);
-                        o[r][4 * e + 2] = fmaf(w, v.z, o[r][4 * e + 2]);
-                        o[r][4 * e + 3] = fmaf(w, v.w, o[r][4 * e + 3]);
+                    for (int h = 0; h < 8; h += 4) {
+                        mma_1688(s[k], qa[h], qb[h], qa[h + 2], qb[h + 2], kk[h], kk[h + 2]);
+                        mma_1688(s[k], qa[h + 1], qb[h + 1], qa[h + 3], qb[h + 3], kk[h], kk[h + 2]);
+                        mma_1688(s[k], qa[h], qb[h], qa[h + 2], qb[h + 2], kk[h + 1], kk[h + 3]);
                     }
                 }
+            }
+        const bool masked = k0 + KT - 1 > pw0 || (a.window > 0 && k0 <= pw1 - a.window);
+        auto seen = [&](int r, int k, int e) {
+            const int tok = k0 + 8 * k + 2 * t + e;
+            return !masked || (tok <= pos[r] && (a.window == 0 || tok > pos[r] - a.window));
+        };
+        bool odd = false;
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) odd = odd || (s[k][e] != s[k][e] && seen(e >> 1, k, e & 1));
+        if (__any_sync(0xffffffffu, odd)) {
+            // The split turns an infinity into NaN: such a tile's scores are
+            // formed again, in FP32.
+#pragma unroll 1
+            for (int i = 0; i < 4 * NT; ++i) {
+                const int tok = 8 * (i >> 2) + 2 * t + (i & 1);
+                float v = 0.0f;
+#pragma unroll 1
+                for (int d = 0; d < D; ++d)
+                    v = fmaf(qr[(i & 2) * 4 * LD + d], *reinterpret_cast<const float *>(stage + (d >> 5) * T::kBoxBytes + tok * 128 +
+                                                                                     ((((d >> 2) & 7) ^ (tok & 7)) << 4) + 4 * (d & 3)), v);
+#pragma unroll
+                for (int k = 0; k < NT; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (4 * k + e == i) s[k][e] = v;
+            }
         }
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[k][e] = a.softcap > 0.0f ? capped_log2<false>(s[k][e], cap) : s[k][e] * (a.scale * kLog2e);
+                if (!seen(e >> 1, k, e & 1)) s[k][e] = -INFINITY;
+                mx[e >> 1] = fmaxf(mx[e >> 1], s[k][e]);
+            }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        }
+        if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+            float f[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float x = fmaxf(m[r], mx[r]);
+                f[r] = x == -INFINITY ? 1.0f : ex2(m[r] - x);
+                m[r] = x;
+                l[r] *= f[r];
+            }
+#pragma unroll
+            for (int x = 0; x < NB; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[x][i][e] *= f[e >> 1];
+        }
+        float w[NT][8];  // (hi, lo) of the four weights
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float v = ex2(s[k][e] - (m[e >> 1] == -INFINITY ? 0.0f : m[e >> 1]));
+                l[e >> 1] += v;
+                split_tf32(v, w[k][2 * e], w[k][2 * e + 1]);
+            }
+        if (k0 < lo || k0 + KT > len) {
+            // rows of V that no row sees may hold NaN: weight 0 would not
+            // silence them (either warp of the tile clears them all)
+            for (int r = 0; r < KT; ++r) {
+                if (k0 + r >= lo && k0 + r < len) continue;
+                for (int ch = lane; ch < D / 4; ch += 32)
+                    *reinterpret_cast<uint4 *>(stage + T::kHalfBytes + (ch >> 3) * T::kBoxBytes + r * 128 + (ch & 7) * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();  // before the stage's next TMA write
+            __syncwarp();
+        }
+        // lane (g, t) reads chunk g of the rows of its two tokens: channel
+        // 4 g + i of a box is column g of the box's MMA i
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+#pragma unroll
+            for (int k = 0; k < NT; ++k) {
+                const unsigned char *vp = stage + T::kHalfBytes + x * T::kBoxBytes + (8 * k + 2 * t) * 128;
+                float v0[8], v1[8];
+                split_tf32(*reinterpret_cast<const float4 *>(vp + ((g ^ (2 * t)) << 4)), v0);
+                split_tf32(*reinterpret_cast<const float4 *>(vp + 128 + ((g ^ (2 * t + 1)) << 4)), v1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mma_1688(o[x][i], w[k][0], w[k][4], w[k][2], w[k][6], v0[2 * i], v1[2 * i]);
+                    mma_1688(o[x][i], w[k][1], w[k][5], w[k][3], w[k][7], v0[2 * i], v1[2 * i]);
+                    mma_1688(o[x][i], w[k][0], w[k][4], w[k][2], w[k][6], v0[2 * i + 1], v1[2 * i + 1]);
+                }
+            }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[kg][st]);
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const float f = 1.0f / group_sum<16>(l[r]);
-        const int row = 4 * rg + r;
-        if (row >= qt.rows) continue;
+    for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    }
+    // join the two halves of the keys: group 1 hands over through shared memory
+    __syncthreads();
+    float *jo = reinterpret_cast<float *>(ring) + rg * 16 * (D + 2);
+    if (kg == 1) {
 #pragma unroll
-        for (int e = 0; e < D / 64; ++e)
+        for (int r = 0; r < 2; ++r) {
+            float *row = jo + (g + 8 * r) * (D + 2);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                store_io<false>(a.o, ((size_t)(qt.base + qt.first + row) * a.Hq + h) * D + 64 * e + 4 * cg + i, o[r][4 * e + i] * f);
+            for (int x = 0; x < NB; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) row[32 * x + 8 * t + 4 * e + i] = o[x][i][2 * r + e];
+            if (t == 0) row[D] = m[r], row[D + 1] = l[r];
+        }
+    }
+    __syncthreads();
+    if (kg == 1 || !ok) return;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int R = 16 * rg + g + 8 * r, tok = R >> group_shift;
+        if (tok >= qt.rows) continue;
+        const float *row = jo + (g + 8 * r) * (D + 2);
+        const float m1 = row[D], top = fmaxf(m[r], m1), base = top == -INFINITY ? 0.0f : top;
+        const float f0 = ex2(m[r] - base), f1 = ex2(m1 - base), f = 1.0f / (l[r] * f0 + row[D + 1] * f1);
+        float *dst = static_cast<float *>(a.o) + ((size_t)(qt.base + qt.first + tok) * a.Hq + h0 + (R & (heads - 1))) * D;
+#pragma unroll
+        for (int x = 0; x < NB; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = (o[x][i][2 * r + e] * f0 + row[32 * x + 8 * t + 4 * e + i] * f1) * f;
+                *reinterpret_cast<float4 *>(dst + 32 * x + 8 * t + 4 * e) = make_float4(v[0], v[1], v[2], v[3]);
+            }
     }
 }
 
+// log2 of the heads that share a block's rows: the power of two in Hq / Hkv, at most 32.
+int group_shift_of(const AttnArgs &a) {
+    int gs = 0;
+    while (gs < 5 && ((a.Hq / a.Hkv) >> gs) % 2 == 0) ++gs;
+    return gs;
+}
+
 template <int D>
-cudaError_t launch_simt(const AttnArgs &a, cudaStream_t stream) {
-    using S = Simt<D>;
+cudaError_t launch_f32(const AttnArgs &a, cudaStream_t stream) {
+    using T = F32<D>;
     static std::atomic<uint64_t> ready{0};
-    auto kern = attn_prefill_simt<D>;
-    const cudaError_t e = allow_smem(kern, ready, S::kSmem);
+    auto kern = attn_prefill_f32<D>;
+    const cudaError_t e = allow_smem(kern, ready, T::kSmem);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)query_tiles(a, S::kRows), (unsigned)a.Hq);
-    kern<<<grid, S::kThreads, S::kSmem, stream>>>(a);
+    const int gs = group_shift_of(a);
+    CUtensorMap km, vm;
+    if (!page_map(&km, a.k_pages, D, a, false, 16) || !page_map(&vm, a.v_pages, D, a, false, 16)) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)query_tiles(a, T::kRows >> gs), (unsigned)(a.Hq >> gs));
+    kern<<<grid, T::kThreads, T::kSmem, stream>>>(km, vm, a, gs);
     return cudaGetLastError();
 }
 
@@ -690,10 +826,8 @@ cudaError_t launch_tc(const AttnArgs &a, cudaStream_t stream) {
     auto kern = attn_prefill_tc<D, CAP>;
     const cudaError_t e = allow_smem(kern, ready, T::kSmem);
     if (e != cudaSuccess) return e;
-    // heads of a block: the power of two in Hq / Hkv, at most 32
-    const int G = a.Hq / a.Hkv;
-    int gs = 0, bs = a.page_shift;
-    while (gs < 5 && (G >> gs) % 2 == 0) ++gs;
+    const int gs = group_shift_of(a);
+    int bs = a.page_shift;
     while ((1 << bs) > T::kKeys) --bs;
     CUtensorMap qm, km, vm;
     if (!query_map(&qm, a, D, 1 << gs) || !page_map(&km, a.k_pages, D, a, true, 1 << bs) ||
@@ -713,9 +847,9 @@ cudaError_t launch_tc_d(const AttnArgs &a, cudaStream_t stream) {
 
 cudaError_t launch_attn_prefill(const AttnArgs &a, int D, bool bf16, cudaStream_t stream) {
     switch (D) {
-        case 64: return bf16 ? launch_tc_d<64>(a, stream) : launch_simt<64>(a, stream);
-        case 128: return bf16 ? launch_tc_d<128>(a, stream) : launch_simt<128>(a, stream);
-        case 256: return bf16 ? launch_tc_d<256>(a, stream) : launch_simt<256>(a, stream);
+        case 64: return bf16 ? launch_tc_d<64>(a, stream) : launch_f32<64>(a, stream);
+        case 128: return bf16 ? launch_tc_d<128>(a, stream) : launch_f32<128>(a, stream);
+        case 256: return bf16 ? launch_tc_d<256>(a, stream) : launch_f32<256>(a, stream);
     }
     return cudaErrorInvalidValue;
 }
