@@ -160,7 +160,7 @@ __device__ __forceinline__ QueryTile find_query_tile(const AttnArgs &a, int rows
         if (start < 0 || base < 0) return 0;
         if (n > a.tokens - base) n = a.tokens - base;
         if (n > (long long)cap - start) {
-            if (tile_index == 0 && blockIdx.y == 0 && n > 0) atomicOr(&g_dev_error, kErrBadPosition);
+            if (tile_index == 0 && n > 0) atomicOr(&g_dev_error, kErrBadPosition);
             n = (long long)cap - start;
         }
         return n > 0 ? (int)n : 0;

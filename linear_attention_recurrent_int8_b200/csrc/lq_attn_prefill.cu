@@ -12,6 +12,18 @@
 namespace lq {
 namespace {
 
+// What a block works on.  Tiles with the most keys before them (the last of a
+// sequence) go first, those of all heads together, so that the last blocks to
+// start are short ones.
+struct BlockPlace {
+    long long tile;
+    int head;  // first of the block's heads
+};
+__device__ __forceinline__ BlockPlace place_of(const AttnArgs &a, int group_shift) {
+    const unsigned groups = (unsigned)a.Hq >> group_shift, tiles = gridDim.x / groups, t = blockIdx.x / groups;
+    return BlockPlace{(long long)(tiles - 1 - t), (int)((blockIdx.x - t * groups) << group_shift)};
+}
+
 // ---------------------------------------------------------------------------
 // FP32: warp MMAs on operands in two TF32 parts
 // ---------------------------------------------------------------------------
@@ -44,12 +56,12 @@ __global__ void __launch_bounds__(F32<D>::kThreads) attn_prefill_f32(const __gri
     float *qs = reinterpret_cast<float *>(ring + 4 * T::kStageBytes);
     __shared__ uint64_t full[2][2], empty[2][2];
     __shared__ int find[T::kThreads / 32 + 6];
-    // the last tiles see the most keys: they go first
-    const QueryTile qt = find_query_tile<T::kThreads>(a, T::kRows >> group_shift, gridDim.x - 1 - (long long)blockIdx.x, find);
+    const BlockPlace at = place_of(a, group_shift);
+    const QueryTile qt = find_query_tile<T::kThreads>(a, T::kRows >> group_shift, at.tile, find);
     if (qt.rows <= 0) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rg = warp & 1, kg = warp >> 1;
-    const int heads = 1 << group_shift, h0 = blockIdx.y << group_shift, kv = h0 / (a.Hq / a.Hkv);
+    const int heads = 1 << group_shift, h0 = at.head, kv = h0 / (a.Hq / a.Hkv);
     const int p0 = qt.start + qt.first, len = p0 + qt.rows;  // keys any row sees: lo .. len - 1
     const int lo = a.window > 0 && p0 + 1 > a.window ? p0 + 1 - a.window : 0;
     const int k_first = lo / KT, n = (len - 1) / KT - k_first + 1;
@@ -113,11 +125,13 @@ __global__ void __launch_bounds__(F32<D>::kThreads) attn_prefill_f32(const __gri
         __syncwarp();
         ok = __all_sync(0xffffffffu, ok && bar_wait(&full[kg][st], (it >> 1) & 1));
         if (!ok) break;
-        float s[NT][4];  // rows g, g (tokens 2t, 2t + 1), g + 8, g + 8
+        // rows g, g (tokens 2t, 2t + 1), g + 8, g + 8; the three products are
+        // summed apart, which keeps three chains of MMAs going per 8 keys
+        float s[NT][4], s1[NT][4], s2[NT][4];
 #pragma unroll
         for (int k = 0; k < NT; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[k][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) s[k][e] = s1[k][e] = s2[k][e] = 0.0f;
         // a lane reads 16 bytes of channels at a time: lane t takes chunks 2t
         // and 2t + 1 of a box as two K steps
 #pragma unroll
@@ -134,11 +148,15 @@ __global__ void __launch_bounds__(F32<D>::kThreads) attn_prefill_f32(const __gri
 #pragma unroll
                     for (int h = 0; h < 8; h += 4) {
                         mma_1688(s[k], qa[h], qb[h], qa[h + 2], qb[h + 2], kk[h], kk[h + 2]);
-                        mma_1688(s[k], qa[h + 1], qb[h + 1], qa[h + 3], qb[h + 3], kk[h], kk[h + 2]);
-                        mma_1688(s[k], qa[h], qb[h], qa[h + 2], qb[h + 2], kk[h + 1], kk[h + 3]);
+                        mma_1688(s1[k], qa[h + 1], qb[h + 1], qa[h + 3], qb[h + 3], kk[h], kk[h + 2]);
+                        mma_1688(s2[k], qa[h], qb[h], qa[h + 2], qb[h + 2], kk[h + 1], kk[h + 3]);
                     }
                 }
             }
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[k][e] += s1[k][e] + s2[k][e];
         const bool masked = k0 + KT - 1 > pw0 || (a.window > 0 && k0 <= pw1 - a.window);
         auto seen = [&](int r, int k, int e) {
             const int tok = k0 + 8 * k + 2 * t + e;
@@ -229,11 +247,11 @@ __global__ void __launch_bounds__(F32<D>::kThreads) attn_prefill_f32(const __gri
                 split_tf32(*reinterpret_cast<const float4 *>(vp + ((g ^ (2 * t)) << 4)), v0);
                 split_tf32(*reinterpret_cast<const float4 *>(vp + 128 + ((g ^ (2 * t + 1)) << 4)), v1);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    mma_1688(o[x][i], w[k][0], w[k][4], w[k][2], w[k][6], v0[2 * i], v1[2 * i]);
-                    mma_1688(o[x][i], w[k][1], w[k][5], w[k][3], w[k][7], v0[2 * i], v1[2 * i]);
-                    mma_1688(o[x][i], w[k][0], w[k][4], w[k][2], w[k][6], v0[2 * i + 1], v1[2 * i + 1]);
-                }
+                for (int i = 0; i < 4; ++i) mma_1688(o[x][i], w[k][0], w[k][4], w[k][2], w[k][6], v0[2 * i], v1[2 * i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mma_1688(o[x][i], w[k][1], w[k][5], w[k][3], w[k][7], v0[2 * i], v1[2 * i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mma_1688(o[x][i], w[k][0], w[k][4], w[k][2], w[k][6], v0[2 * i + 1], v1[2 * i + 1]);
             }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[kg][st]);
@@ -298,7 +316,7 @@ cudaError_t launch_f32(const AttnArgs &a, cudaStream_t stream) {
     const int gs = group_shift_of(a);
     CUtensorMap km, vm;
     if (!page_map(&km, a.k_pages, D, a, false, 16) || !page_map(&vm, a.v_pages, D, a, false, 16)) return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)query_tiles(a, T::kRows >> gs), (unsigned)(a.Hq >> gs));
+    const unsigned grid = (unsigned)(query_tiles(a, T::kRows >> gs) * (a.Hq >> gs));
     kern<<<grid, T::kThreads, T::kSmem, stream>>>(km, vm, a, gs);
     return cudaGetLastError();
 }
@@ -470,10 +488,10 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     __shared__ int find[T::kThreads / 32 + 6];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tokens = 128 * NS >> group_shift;  // of a block
-    // the last tiles see the most keys: they go first
-    const QueryTile qt = find_query_tile<T::kThreads>(a, tokens, gridDim.x - 1 - (long long)blockIdx.x, find);
+    const BlockPlace at = place_of(a, group_shift);
+    const QueryTile qt = find_query_tile<T::kThreads>(a, tokens, at.tile, find);
     if (qt.rows <= 0) return;
-    const int h0 = blockIdx.y << group_shift, kv = h0 / (a.Hq / a.Hkv);
+    const int h0 = at.head, kv = h0 / (a.Hq / a.Hkv);
     const int p0 = qt.start + qt.first, len = p0 + qt.rows;  // keys any row sees: lo .. len - 1
     const int lo = a.window > 0 && p0 + 1 > a.window ? p0 + 1 - a.window : 0;
     // (a second stream without rows is left out)
@@ -833,7 +851,7 @@ cudaError_t launch_tc(const AttnArgs &a, cudaStream_t stream) {
     if (!query_map(&qm, a, D, 1 << gs) || !page_map(&km, a.k_pages, D, a, true, 1 << bs) ||
         !page_map(&vm, a.v_pages, D, a, true, 1 << bs))
         return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)query_tiles(a, 128 * T::kStreams >> gs), (unsigned)(a.Hq >> gs));
+    const unsigned grid = (unsigned)(query_tiles(a, 128 * T::kStreams >> gs) * (a.Hq >> gs));
     kern<<<grid, T::kThreads, T::kSmem, stream>>>(qm, km, vm, a, gs, bs);
     return cudaGetLastError();
 }
