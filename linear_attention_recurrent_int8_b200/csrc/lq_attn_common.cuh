@@ -165,12 +165,15 @@ __device__ __forceinline__ QueryTile find_query_tile(const AttnArgs &a, int rows
         }
         return n > 0 ? (int)n : 0;
     };
+    // a thread's sequences; with at most NT of them it keeps what it read
     const int chunk = (a.B + NT - 1) / NT;
-    long long base;
-    int start, mine = 0;
+    long long base = 0;
+    int start = 0, mine = 0, n = 0;
     for (int i = 0; i < chunk; ++i) {
         const int b = tid * chunk + i;
-        if (b < a.B) mine += (rows_of(b, base, start) + rows - 1) / rows;
+        if (b >= a.B) break;
+        n = rows_of(b, base, start);
+        mine += (n + rows - 1) / rows;
     }
     int incl = mine;
 #pragma unroll
@@ -187,8 +190,8 @@ __device__ __forceinline__ QueryTile find_query_tile(const AttnArgs &a, int rows
     if (tile_index >= at && tile_index < at + mine) {
         for (int i = 0; i < chunk; ++i) {
             const int b = tid * chunk + i;
-            if (b >= a.B) break;
-            const int n = rows_of(b, base, start), t = (n + rows - 1) / rows;
+            if (chunk > 1) n = rows_of(b, base, start);
+            const int t = (n + rows - 1) / rows;
             if (tile_index < at + t) {
                 const int first = (int)(tile_index - at) * rows;
                 found[0] = b;

@@ -404,14 +404,23 @@ __device__ __forceinline__ void ex2_fma(f32x2 v, float &a, float &b) {
     b = __int_as_float(__float_as_int(pb) + (int)((unsigned)__float_as_int(tb) << 23));
 }
 
-// tanh y of two values, |y| <= 1: y + y^3 times a cubic in y^2 (least maximum
-// error, 4.1e-6).
-__device__ __forceinline__ f32x2 tanh_fma(f32x2 y) {
-    const f32x2 u = mul2(y, y);
-    f32x2 p = fma2(u, two(0.008854211308062077f, 0.008854211308062077f), two(-0.04448200762271881f, -0.04448200762271881f));
-    p = fma2(p, u, two(0.13020214438438416f, 0.13020214438438416f));
-    p = fma2(p, u, two(-0.3329765796661377f, -0.3329765796661377f));
-    return fma2(mul2(y, u), p, y);
+// cap tanh(z x) in units of log2 for |z x| <= 3/4, as x times a polynomial in
+// x^2 whose coefficients hold z and the cap: tanh y = y + y^3 (c0 + c1 y^2 +
+// c2 y^4), least maximum error 5.6e-6.
+constexpr float kTanhReach = 0.75f;
+struct CapPoly {
+    float k[4];
+};
+__device__ __forceinline__ CapPoly cap_poly(float z, float out) {
+    const float z3 = z * z * z, z5 = z3 * z * z, z7 = z5 * z * z;
+    return CapPoly{{out * z, out * z3 * -0.3327198326587677f, out * z5 * 0.1272989809513092f, out * z7 * -0.03519973158836365f}};
+}
+__device__ __forceinline__ f32x2 capped(f32x2 x, const CapPoly &c) {
+    const f32x2 u = mul2(x, x);
+    f32x2 p = fma2(u, two(c.k[3], c.k[3]), two(c.k[2], c.k[2]));
+    p = fma2(p, u, two(c.k[1], c.k[1]));
+    p = fma2(p, u, two(c.k[0], c.k[0]));
+    return mul2(p, x);
 }
 
 // Shared-memory operand descriptors as two words: all K steps of a tile share
@@ -488,9 +497,13 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     __shared__ int find[T::kThreads / 32 + 6];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tokens = 128 * NS >> group_shift;  // of a block
+    if (warp == T::kMmaWarp) tmem_alloc(&tmem_slot, T::kCols);
     const BlockPlace at = place_of(a, group_shift);
     const QueryTile qt = find_query_tile<T::kThreads>(a, tokens, at.tile, find);
-    if (qt.rows <= 0) return;
+    if (qt.rows <= 0) {
+        if (warp == T::kMmaWarp) tmem_dealloc(tmem_slot, T::kCols);
+        return;
+    }
     const int h0 = at.head, kv = h0 / (a.Hq / a.Hkv);
     const int p0 = qt.start + qt.first, len = p0 + qt.rows;  // keys any row sees: lo .. len - 1
     const int lo = a.window > 0 && p0 + 1 > a.window ? p0 + 1 - a.window : 0;
@@ -508,7 +521,6 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         }
         mbar_init(&bars.tail, 1);
     }
-    if (warp == T::kMmaWarp) tmem_alloc(&tmem_slot, T::kCols);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -692,7 +704,8 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
         // masked score stays -inf), or 1 for capped scores
         const float c = CAP ? 1.0f : fmaxf(fabsf(a.scale * kLog2e), 1e-30f);
         const SoftCap cap = soft_cap<true>(a.scale, a.softcap);
-        const float cap_in = a.scale / a.softcap, in_reach = 1.0f / fabsf(cap_in);
+        const CapPoly poly = cap_poly(a.scale / a.softcap, cap.out);
+        const float in_reach = kTanhReach * a.softcap / fabsf(a.scale);
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int j = 0; j < n; ++j) {
@@ -705,13 +718,15 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
             if constexpr (CAP) {
                 // scores well inside the cap, as they mostly are, take a
                 // polynomial on the FMA pipe; two special functions else
-                float big = 0.0f;
+                float big0 = 0.0f, big1 = 0.0f;
 #pragma unroll
-                for (int i = 0; i < KT; i += 2) big = max3(big, fabsf(x[i]), fabsf(x[i + 1]));
-                if (__all_sync(0xffffffffu, big <= in_reach)) {
+                for (int i = 0; i < KT; i += 4) {
+                    big0 = max3(big0, fabsf(x[i]), fabsf(x[i + 1]));
+                    big1 = max3(big1, fabsf(x[i + 2]), fabsf(x[i + 3]));
+                }
+                if (__all_sync(0xffffffffu, big0 <= in_reach && big1 <= in_reach)) {
 #pragma unroll
-                    for (int i = 0; i < KT; i += 2)
-                        apart(mul2(tanh_fma(mul2(two(x[i], x[i + 1]), two(cap_in, cap_in))), two(cap.out, cap.out)), x[i], x[i + 1]);
+                    for (int i = 0; i < KT; i += 2) apart(capped(two(x[i], x[i + 1]), poly), x[i], x[i + 1]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < KT; ++i) x[i] = capped_log2<true>(x[i], cap);
@@ -721,11 +736,15 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
                 for (int i = 0; i < KT; ++i) x[i] = -x[i];
             }
             const int k0 = (k_first + j) * KT;
-            if (k0 + KT - 1 > pw0 || (a.window > 0 && k0 <= pw1 - a.window)) {
-                const int hi = p - k0, first = a.window > 0 ? hi - a.window + 1 : 0;
+            if (k0 + KT - 1 > pw0) {
+                const int hi = p - k0;
 #pragma unroll
-                for (int i = 0; i < KT; ++i)
-                    if (i > hi || i < first) x[i] = -INFINITY;
+                for (int i = 0; i < KT; ++i) x[i] = i > hi ? -INFINITY : x[i];
+            }
+            if (a.window > 0 && k0 <= pw1 - a.window) {
+                const int first = p - a.window + 1 - k0;
+#pragma unroll
+                for (int i = 0; i < KT; ++i) x[i] = i < first ? -INFINITY : x[i];
             }
             float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
