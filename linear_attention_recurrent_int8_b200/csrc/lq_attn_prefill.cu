@@ -511,15 +511,10 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     const int streams = NS == 2 && qt.rows > tokens / 2 ? 2 : 1;
     const int k_first = lo / KT, n = (len - 1) / KT - k_first + 1;
 
-    if (tid == 0) {
-        mbar_init(&bars.q_full, 1);
-        for (int i = 0; i < T::kSlots; ++i) mbar_init(&bars.kv_full[i], 1), mbar_init(&bars.kv_empty[i], 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.s_full[2 * i], 1), mbar_init(&bars.s_full[2 * i + 1], 1);
-            mbar_init(&bars.o_done[i], 1);
-            mbar_init(&bars.p_half[i], 4), mbar_init(&bars.p_ready[i], 4);
-        }
-        mbar_init(&bars.tail, 1);
+    if (tid < (int)(sizeof(TcBars) / sizeof(uint64_t))) {
+        // a thread per barrier (each initialisation ends in a fence)
+        uint64_t *bar = reinterpret_cast<uint64_t *>(&bars) + tid;
+        mbar_init(bar, bar == &bars.p_half[0] || bar == &bars.p_half[1] || bar == &bars.p_ready[0] || bar == &bars.p_ready[1] ? 4 : 1);
     }
     tc_fence_before_sync();
     __syncthreads();
