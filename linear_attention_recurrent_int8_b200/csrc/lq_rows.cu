@@ -129,27 +129,31 @@ __global__ void __launch_bounds__(256, NR == 4 ? 4 : 6) rows_kernel(const RowsAr
     long long p = 0;
     size_t page_row = 0;  // row of the token in head 0 of its page
     if constexpr (APPEND) {
-        int b;
+        int b, first;
         long long i;
         if (a.cu) {
-            // sequences whose first row is at or before t
-            int n = 0;
-            for (int j0 = 0; j0 <= a.B; j0 += blockDim.x) {
-                const int j = j0 + tid;
-                n += __syncthreads_count(j <= a.B && __ldg(a.cu + j) <= t);
+            // the sequence that holds row t: its thread has read all that is
+            // needed of it
+            __shared__ int found[3];
+            bool here = false;
+            for (int j = tid; j < a.B; j += blockDim.x) {
+                const int c0 = __ldg(a.cu + j), c1 = __ldg(a.cu + j + 1), f = __ldg(a.pos + j);
+                if (c0 <= t && t < c1) {
+                    here = true;
+                    found[0] = j, found[1] = (int)t - c0, found[2] = f;
+                }
             }
-            b = n - 1;
-            if (b < 0 || b >= a.B) return;  // padding behind the last sequence
-            i = t - __ldg(a.cu + b);
+            if (__syncthreads_count(here) == 0) return;  // padding behind the last sequence
+            b = found[0], i = found[1], first = found[2];
         } else {
             const int per = a.tokens / a.B;
             b = (int)(t / per);
             i = t - (long long)b * per;
+            first = __ldg(a.pos + b);
         }
-        const int first = __ldg(a.pos + b);
         if (first < 0) return;  // idle slot
         p = first + i;
-        const bool bad_pos = i < 0 || p >= (long long)a.max_pages * a.page_size || (a.rot > 0 && p >= a.table_len);
+        const bool bad_pos = p < 0 || p >= (long long)a.max_pages * a.page_size || (a.rot > 0 && p >= a.table_len);
         int page = 0;
         if (!bad_pos) page = __ldg(a.block_table + (size_t)b * a.max_pages + (int)(p >> a.page_shift));
         const bool bad_page = page < 0 || page >= a.num_pages;
