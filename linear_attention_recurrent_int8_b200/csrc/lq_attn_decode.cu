@@ -626,53 +626,115 @@ __global__ void __launch_bounds__(Tile<D, BF16>::kWarps * 32, 1)
     }
 }
 
-// Joins the parts of one query head: block (sequence, head).  Threads take the
-// parts in a fixed pattern and are summed in a fixed order.
-template <int D, bool BF16, int RU>
+// The parts of one query head's output.
+struct JoinJob {
+    int b, head, row, first, parts;  // sequence, head, its row of the group, first worker, number of parts
+};
+
+template <int RU>
+__device__ __forceinline__ JoinJob join_job(const AttnArgs &a, const DecodePlan &pl, long long job) {
+    JoinJob j{};
+    if (job >= (long long)a.B * a.Hq) return j;
+    j.b = (int)(job / a.Hq), j.head = (int)(job - (long long)j.b * a.Hq);
+    const int *h = reinterpret_cast<const int *>(a.ws);
+    const int p0 = h[j.b], n = h[j.b + 1] - p0, per = h[a.B + 1];
+    if (n == 0) return j;
+    const int G = a.Hq / a.Hkv, kv = j.head / G, in = j.head - kv * G;
+    j.row = in % RU;
+    const long long s0 = (long long)p0 * pl.units + (long long)(kv * pl.per_kv + in / RU) * n;
+    j.first = (int)(s0 / per);
+    j.parts = (int)((s0 + n - 1) / per) - j.first + 1;
+    return j;
+}
+
+template <int D, int RU>
+__device__ __forceinline__ const float *join_part(const AttnArgs &a, const JoinJob &j, int i) {
+    // the first part is in its worker's second slot, the others in their worker's first
+    return reinterpret_cast<const float *>(a.ws + ws_header(a.B)) + ((size_t)(j.first + i) * 2 + (i == 0)) * part_floats<D, RU>();
+}
+
+// Joins the parts of the query heads, each sum in a fixed order.  A block takes
+// JB heads: with 8, each warp joins the few parts of a head by itself, and the
+// block comes together for heads of many; with 1 the block joins one head.  A
+// head whose pair lay in one run was written by its worker.
+template <int D, bool BF16, int RU, int JB>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, const DecodePlan pl) {
-    constexpr int LR = D / 4, NG = 256 / LR;  // lanes of a row, parts taken at a time
+    constexpr int LR = D / 4, NG = 256 / LR;  // lanes of a row, parts taken at a time by the block
+    constexpr int kFew = JB == 1 ? 1 : 16;    // parts up to which a warp works alone
+    constexpr int NV = D / 32;                // channels of a lane of a lone warp
     __shared__ float red[8];
     __shared__ __align__(16) float acc[NG][D];
     __shared__ float sums[NG];
-    const int tid = threadIdx.x, b = blockIdx.x / a.Hq, head = blockIdx.x % a.Hq;
-    const int G = a.Hq / a.Hkv, in = head % G;
-    const int u = head / G * pl.per_kv + in / RU, row = in % RU;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
-    const int *h = reinterpret_cast<const int *>(a.ws);
-    const int p0 = h[b], n = h[b + 1] - p0, per = h[a.B + 1];
-    if (n == 0) return;
-    const long long s0 = (long long)p0 * pl.units + (long long)u * n;
-    const int w0 = (int)(s0 / per), parts = (int)((s0 + n - 1) / per) - w0 + 1;
-    if (parts == 1) return;  // written by its worker
-    const float *ws = reinterpret_cast<const float *>(a.ws + ws_header(a.B));
-    auto part_of = [&](int i) { return ws + ((size_t)(w0 + i) * 2 + (i == 0)) * part_floats<D, RU>(); };
-    float m = -INFINITY;
-    for (int i = tid; i < parts; i += 256) m = fmaxf(m, part_of(i)[RU * D + 2 * row]);
-    m = group_max<32>(m);
-    if ((tid & 31) == 0) red[tid >> 5] = m;
-    __syncthreads();
+    const JoinJob mine = join_job<RU>(a, pl, (long long)blockIdx.x * JB + (JB == 1 ? 0 : warp));
+    if (mine.parts > 1 && mine.parts <= kFew) {
+        const int x = lane < mine.parts ? lane : 0;
+        const float2 ml = *reinterpret_cast<const float2 *>(join_part<D, RU>(a, mine, x) + RU * D + 2 * mine.row);
+        float m = group_max<32>(ml.x);
+        if (m == -INFINITY) m = 0.0f;
+        const float f = lane < mine.parts ? ex2(ml.x - m) : 0.0f;
+        float sum = 0.0f, o[NV];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
-    if (m == -INFINITY) m = 0.0f;
-    const int g = tid / LR, c = 4 * (tid % LR);
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float sum = 0.0f;
-    for (int i = g; i < parts; i += NG) {
-        const float *p = part_of(i);
-        const float2 ml = *reinterpret_cast<const float2 *>(p + RU * D + 2 * row);
-        const float4 v = *reinterpret_cast<const float4 *>(p + row * D + c);
-        const float f = ex2(ml.x - m);
-        sum = fmaf(ml.y, f, sum);
-        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+        for (int e = 0; e < NV; ++e) o[e] = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < mine.parts; ++i) {
+            const float w = __shfl_sync(0xffffffffu, f, i), l = __shfl_sync(0xffffffffu, ml.y, i);
+            const float *p = join_part<D, RU>(a, mine, i) + mine.row * D + NV * lane;
+            sum = fmaf(l, w, sum);
+#pragma unroll
+            for (int e = 0; e < NV; e += 2) {
+                const float2 v = *reinterpret_cast<const float2 *>(p + e);
+                o[e] = fmaf(v.x, w, o[e]), o[e + 1] = fmaf(v.y, w, o[e + 1]);
+            }
+        }
+        const size_t at = ((size_t)mine.b * a.Hq + mine.head) * D + NV * lane;
+#pragma unroll
+        for (int e = 0; e < NV; ++e) store_io<BF16>(a.o, at + e, o[e] / sum);
     }
-    *reinterpret_cast<float4 *>(&acc[g][c]) = o;
-    if (c == 0) sums[g] = sum;
-    __syncthreads();
-    if (tid < D) {
-        float x = 0.0f, s = 0.0f;
+    unsigned many = 1;
+    if (JB > 1) {
+        // which heads the block joins together
+        if (lane == 0) red[warp] = mine.parts > kFew ? 1.0f : 0.0f;
+        if (!__syncthreads_or(mine.parts > kFew)) return;
+        many = 0;
+        for (int w = 0; w < 8; ++w) many |= (red[w] != 0.0f ? 1u : 0u) << w;
+        __syncthreads();
+    } else if (mine.parts <= 1) {
+        return;
+    }
+    for (; many; many &= many - 1) {
+        const JoinJob j = JB == 1 ? mine : join_job<RU>(a, pl, (long long)blockIdx.x * JB + __ffs(many) - 1);
+        float m = -INFINITY;
+        for (int i = tid; i < j.parts; i += 256) m = fmaxf(m, join_part<D, RU>(a, j, i)[RU * D + 2 * j.row]);
+        m = group_max<32>(m);
+        if (lane == 0) red[warp] = m;
+        __syncthreads();
 #pragma unroll
-        for (int k = 0; k < NG; ++k) x += acc[k][tid], s += sums[k];
-        store_io<BF16>(a.o, ((size_t)b * a.Hq + head) * D + tid, x / s);
+        for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
+        if (m == -INFINITY) m = 0.0f;
+        const int g = tid / LR, c = 4 * (tid % LR);
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float sum = 0.0f;
+#pragma unroll 4
+        for (int i = g; i < j.parts; i += NG) {
+            const float *p = join_part<D, RU>(a, j, i);
+            const float2 ml = *reinterpret_cast<const float2 *>(p + RU * D + 2 * j.row);
+            const float4 v = *reinterpret_cast<const float4 *>(p + j.row * D + c);
+            const float f = ex2(ml.x - m);
+            sum = fmaf(ml.y, f, sum);
+            o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+        }
+        *reinterpret_cast<float4 *>(&acc[g][c]) = o;
+        if (c == 0) sums[g] = sum;
+        __syncthreads();
+        if (tid < D) {
+            float x = 0.0f, s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NG; ++k) x += acc[k][tid], s += sums[k];
+            store_io<BF16>(a.o, ((size_t)j.b * a.Hq + j.head) * D + tid, x / s);
+        }
+        __syncthreads();
     }
 }
 
@@ -702,7 +764,10 @@ cudaError_t launch_decode_ru(const AttnArgs &a, cudaStream_t stream) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)a.B * a.Hq);
+    // a block per head while they fill the GPU about once, else one for 8
+    const int jobs = a.B * a.Hq;
+    const bool few = jobs <= pl.workers;
+    cfg.gridDim = dim3((unsigned)(few ? jobs : (jobs + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
@@ -710,7 +775,8 @@ cudaError_t launch_decode_ru(const AttnArgs &a, cudaStream_t stream) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, BF16, RU>, a, pl);
+    if (few) return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, BF16, RU, 1>, a, pl);
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, BF16, RU, 8>, a, pl);
 }
 
 template <int D, bool BF16>
