@@ -37,7 +37,7 @@ namespace {
 template <int D, bool BF16>
 struct Tile {
     static constexpr int kTok = BF16 || D == 64 ? 16 : 8;       // tokens of a tile
-    static constexpr int kWarps = D < 256 ? 8 : 4;              // warps of a block
+    static constexpr int kWarps = 8;                            // warps of a block
     static constexpr int kRowEl = BF16 ? 64 : 32;               // elements of a 128-byte box row
     static constexpr int kBoxes = D / kRowEl;                   // boxes of a tile of K (or V)
     static constexpr int kBoxBytes = kTok * 128;
@@ -655,20 +655,22 @@ __device__ __forceinline__ const float *join_part(const AttnArgs &a, const JoinJ
 
 // Joins the parts of the query heads, each sum in a fixed order.  A block takes
 // JB heads: with 8, each warp joins the few parts of a head by itself, and the
-// block comes together for heads of many; with 1 the block joins one head.  A
-// head whose pair lay in one run was written by its worker.
+// block comes together for heads of many; with 1 the block joins 64 channels
+// of one head (a few long sequences leave hundreds of parts per head).  A head
+// whose pair lay in one run was written by its worker.
 template <int D, bool BF16, int RU, int JB>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, const DecodePlan pl) {
-    constexpr int LR = D / 4, NG = 256 / LR;  // lanes of a row, parts taken at a time by the block
+    constexpr int NC = JB == 1 ? 64 : D, LR = NC / 4, NG = 256 / LR;  // channels of the block, their lanes, parts taken at a time
     constexpr int kFew = JB == 1 ? 1 : 16;    // parts up to which a warp works alone
     constexpr int NV = D / 32;                // channels of a lane of a lone warp
     __shared__ float red[8];
-    __shared__ __align__(16) float acc[NG][D];
+    __shared__ __align__(16) float acc[NG][NC];
     __shared__ float sums[NG];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
-    const JoinJob mine = join_job<RU>(a, pl, (long long)blockIdx.x * JB + (JB == 1 ? 0 : warp));
-    if (mine.parts > 1 && mine.parts <= kFew) {
+    const JoinJob mine = join_job<RU>(a, pl, JB == 1 ? blockIdx.x / (D / NC) : (long long)blockIdx.x * JB + warp);
+    const int c0 = JB == 1 ? blockIdx.x % (D / NC) * NC : 0;
+    if (JB > 1 && mine.parts > 1 && mine.parts <= kFew) {
         const int x = lane < mine.parts ? lane : 0;
         const float2 ml = *reinterpret_cast<const float2 *>(join_part<D, RU>(a, mine, x) + RU * D + 2 * mine.row);
         float m = group_max<32>(ml.x);
@@ -720,7 +722,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, const 
         for (int i = g; i < j.parts; i += NG) {
             const float *p = join_part<D, RU>(a, j, i);
             const float2 ml = *reinterpret_cast<const float2 *>(p + RU * D + 2 * j.row);
-            const float4 v = *reinterpret_cast<const float4 *>(p + j.row * D + c);
+            const float4 v = *reinterpret_cast<const float4 *>(p + j.row * D + c0 + c);
             const float f = ex2(ml.x - m);
             sum = fmaf(ml.y, f, sum);
             o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
@@ -728,11 +730,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, const 
         *reinterpret_cast<float4 *>(&acc[g][c]) = o;
         if (c == 0) sums[g] = sum;
         __syncthreads();
-        if (tid < D) {
+        if (tid < NC) {
             float x = 0.0f, s = 0.0f;
 #pragma unroll
             for (int k = 0; k < NG; ++k) x += acc[k][tid], s += sums[k];
-            store_io<BF16>(a.o, ((size_t)j.b * a.Hq + j.head) * D + tid, x / s);
+            store_io<BF16>(a.o, ((size_t)j.b * a.Hq + j.head) * D + c0 + tid, x / s);
         }
         __syncthreads();
     }
@@ -767,7 +769,7 @@ cudaError_t launch_decode_ru(const AttnArgs &a, cudaStream_t stream) {
     // a block per head while they fill the GPU about once, else one for 8
     const int jobs = a.B * a.Hq;
     const bool few = jobs <= pl.workers;
-    cfg.gridDim = dim3((unsigned)(few ? jobs : (jobs + 7) / 8));
+    cfg.gridDim = dim3((unsigned)(few ? jobs * (D / 64) : (jobs + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
