@@ -63,6 +63,13 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
     }
 }
 
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
+
 // Box load of a 3-D map ([pages * heads][page_size][D]; no multicast).  A
 // coordinate outside the map fills zeros.
 __device__ __forceinline__ void tma_page_load(void *dst, const CUtensorMap *map, int c0, int c1, int c2,
@@ -72,6 +79,18 @@ __device__ __forceinline__ void tma_page_load(void *dst, const CUtensorMap *map,
         "%4}], [%5];" ::"r"(smem_u32(dst)),
         "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
         : "memory");
+}
+
+// The same with shared-memory addresses, and the bytes that a barrier expects.
+__device__ __forceinline__ void tma_page_load_at(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+    asm volatile("{ .reg .b64 st; mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {

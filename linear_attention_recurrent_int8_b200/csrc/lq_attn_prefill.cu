@@ -424,13 +424,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
         : "memory");
 }
 
-// One lane of the (converged) warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
-    return r != 0;
-}
-
 template <int D>
 struct Tc {
     static constexpr int kStreams = D == 256 ? 1 : 2;     // query tiles of 128 rows
