@@ -81,6 +81,11 @@ __device__ __forceinline__ void tma_page_load(void *dst, const CUtensorMap *map,
         : "memory");
 }
 
+// Brings a map near before its first use.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // The same with shared-memory addresses, and the bytes that a barrier expects.
 __device__ __forceinline__ void tma_page_load_at(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar) {
     asm volatile(

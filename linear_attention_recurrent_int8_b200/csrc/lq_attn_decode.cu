@@ -513,6 +513,7 @@ __global__ void __launch_bounds__(Tile<D, BF16>::kWarps * 32, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     pdl_release();
+    if (tid == 0) prefetch_map(&kmap), prefetch_map(&vmap);
     // lengths and the prefix sums of tiles per pair
     const int cap = a.max_pages << a.page_shift;
     const int chunk = (a.B + NW * 32 - 1) / (NW * 32);
@@ -571,7 +572,11 @@ __global__ void __launch_bounds__(Tile<D, BF16>::kWarps * 32, 1)
     auto page_of = [&](const Cursor &k) -> int {
         return k.b < a.B ? __ldg(a.block_table + (size_t)k.b * a.max_pages + (((k.t0 + k.t) * TOK) >> a.page_shift)) : 0;
     };
-    int page = page_of(pc), fill = 0, filled = 0;
+    // (of the first tiles all at once, lane i of the run's i-th)
+    Cursor ahead = pc;
+    for (int i = 0; i < lane && i < pl.stages && i < run; ++i) advance<TOK>(ahead, len, a.B, pl.units, a.window);
+    const int first_pages = page_of(ahead);
+    int page = 0, fill = 0, filled = 0;
     // The whole warp prepares a tile's copies from values that the compiler
     // knows to be uniform (shuffled from lane 0) and one lane issues them;
     // prepared inside that lane's branch they took about 900 cycles a tile.
@@ -593,26 +598,29 @@ __global__ void __launch_bounds__(Tile<D, BF16>::kWarps * 32, 1)
         }
         __syncwarp();
         if (++fill == pl.stages) fill = 0;
-        if (++filled < run) {
-            advance<TOK>(pc, len, a.B, pl.units, a.window);
-            page = page_of(pc);
-        }
+        if (++filled < run) advance<TOK>(pc, len, a.B, pl.units, a.window);
     };
-    while (filled < run && filled < pl.stages) issue();
 
     typename CoreOf<D, BF16, RU>::type core;
     int st = 0, ph = 0;
-    bool fresh = true, whole = false;  // whole: the run holds the pair's first tile
+    bool fresh = false, whole = false;  // whole: the run holds the pair's first tile
     int head0 = 0, rows = 0;
+    auto begin = [&]() {
+        const int kv = c.u / pl.per_kv, first = (c.u - kv * pl.per_kv) * RU;
+        head0 = kv * G + first;
+        rows = min(RU, G - first);
+        core.begin(a, c.b, head0, rows, lane, sc);
+        whole = c.t == 0;
+        fresh = false;
+    };
+    while (filled < run && filled < pl.stages) {
+        page = __shfl_sync(0xffffffffu, first_pages, filled);
+        issue();
+    }
+    if (filled < run) page = page_of(pc);
+    begin();
     for (int i = 0; i < run; ++i) {
-        if (fresh) {
-            const int kv = c.u / pl.per_kv, first = (c.u - kv * pl.per_kv) * RU;
-            head0 = kv * G + first;
-            rows = min(RU, G - first);
-            core.begin(a, c.b, head0, rows, lane, sc);
-            whole = c.t == 0;
-            fresh = false;
-        }
+        if (fresh) begin();
         if (!bar_wait(full + st, ph)) {
             // give the copies still in flight their time before the block's shared memory is freed
             for (int k = i + 1; k < filled; ++k) {
@@ -624,7 +632,10 @@ __global__ void __launch_bounds__(Tile<D, BF16>::kWarps * 32, 1)
         unsigned char *stage = my_ring + st * T::kStageBytes;
         core.tile(a, stage, (c.t0 + c.t) * TOK, c.lo, c.len, lane, sc, c.b, head0, rows);
         __syncwarp();
-        if (filled < run) issue();
+        if (filled < run) {
+            issue();
+            if (filled < run) page = page_of(pc);
+        }
         if (++st == pl.stages) st = 0, ph ^= 1;
         const bool last = c.t + 1 == c.n;
         if (last || i + 1 == run) {

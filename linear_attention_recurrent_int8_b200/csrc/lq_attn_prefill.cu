@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tokens = 128 * NS >> group_shift;  // of a block
     if (warp == T::kMmaWarp) tmem_alloc(&tmem_slot, T::kCols);
+    if (tid == 0) prefetch_map(&qmap), prefetch_map(&kmap), prefetch_map(&vmap);
     const BlockPlace at = place_of(a, group_shift);
     const QueryTile qt = find_query_tile<T::kThreads>(a, tokens, at.tile, find);
     if (qt.rows <= 0) {
