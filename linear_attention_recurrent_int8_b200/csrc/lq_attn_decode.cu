@@ -307,7 +307,7 @@ struct F32Core {
     static constexpr int TOK = T::kTok, NT = TOK / 8, NB = T::kBoxes;
     static constexpr bool kKeepQ = D < 256;  // split query rows in registers, else FP32 rows in scratch
     float q[kKeepQ ? NB : 1][2][8];
-    float o[NB][4][4], m, l;
+    float o[NB][4][2], m, l;
 
     __device__ __forceinline__ static void mma(float (&d)[4], const float *a, float b0, float b1) {
         mma_1688(d, a[0], a[1], a[2], a[3], b0, b1);
@@ -337,9 +337,7 @@ struct F32Core {
 #pragma unroll
         for (int x = 0; x < NB; ++x)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[x][i][e] = 0.0f;
+            for (int i = 0; i < 4; ++i) o[x][i][0] = o[x][i][1] = 0.0f;
         m = -INFINITY, l = 0.0f;
     }
 
@@ -348,11 +346,14 @@ struct F32Core {
         const int g = lane >> 2, t = lane & 3;
         float s[NT][2];  // scores of tokens 8 n + 2 t, 8 n + 2 t + 1 with row g
         {
-            float c[NT][4];
+            // four chains of MMAs per 8 tokens
+            float c[NT][4][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) c[n][e] = 0.0f;
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[n][i][e] = 0.0f;
 #pragma unroll
             for (int x = 0; x < NB; ++x)
 #pragma unroll
@@ -368,14 +369,18 @@ struct F32Core {
                     for (int n = 0; n < NT; ++n) {
                         float k[8];
                         split_tf32(*reinterpret_cast<const float4 *>(st + x * T::kBoxBytes + (8 * n + g) * 128 + (((2 * t + j) ^ g) << 4)), k);
-                        mma(c[n], qv, k[0], k[2]);
-                        mma(c[n], qv, k[1], k[3]);
-                        mma(c[n], qv + 4, k[4], k[6]);
-                        mma(c[n], qv + 4, k[5], k[7]);
+                        mma(c[n][0], qv, k[0], k[2]);
+                        mma(c[n][1], qv, k[1], k[3]);
+                        mma(c[n][2], qv + 4, k[4], k[6]);
+                        mma(c[n][3], qv + 4, k[5], k[7]);
                     }
                 }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) s[n][0] = c[n][0] + c[n][2], s[n][1] = c[n][1] + c[n][3];
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    s[n][e] = (c[n][0][e] + c[n][2][e]) + ((c[n][1][e] + c[n][3][e]) + (c[n][0][e + 2] + c[n][2][e + 2]) +
+                                                           (c[n][1][e + 2] + c[n][3][e + 2]));
         }
         const bool part = tok0 + TOK > len || tok0 < lo;
         bool seen[NT][2], odd = false;
@@ -426,9 +431,7 @@ struct F32Core {
 #pragma unroll
             for (int x = 0; x < NB; ++x)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[x][i][e] *= f;
+                for (int i = 0; i < 4; ++i) o[x][i][0] *= f, o[x][i][1] *= f;
         }
         const float base = m == -INFINITY ? 0.0f : m;
         float p[NT][4];
@@ -453,7 +456,12 @@ struct F32Core {
         // lane (g, t) reads chunk g of the rows of its two tokens: channel
         // 4 g + i of a box is column g of the box's MMA i
 #pragma unroll
-        for (int x = 0; x < NB; ++x)
+        for (int x = 0; x < NB; ++x) {
+            float c[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[i][e] = 0.0f;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const unsigned char *vp = st + T::kHalfBytes + x * T::kBoxBytes + (8 * n + 2 * t) * 128;
@@ -462,10 +470,13 @@ struct F32Core {
                 split_tf32(*reinterpret_cast<const float4 *>(vp + 128 + ((g ^ (2 * t + 1)) << 4)), v1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    mma(o[x][i], p[n], v0[2 * i], v1[2 * i]);
-                    mma(o[x][i], p[n], v0[2 * i + 1], v1[2 * i + 1]);
+                    mma(c[i], p[n], v0[2 * i], v1[2 * i]);
+                    mma(c[i], p[n], v0[2 * i + 1], v1[2 * i + 1]);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[x][i][0] += c[i][0] + c[i][2], o[x][i][1] += c[i][1] + c[i][3];
+        }
     }
 
     __device__ __forceinline__ void end(const AttnArgs &a, int b, int head0, int rows, float *part, int lane,
@@ -482,8 +493,7 @@ struct F32Core {
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 *reinterpret_cast<float4 *>(dst + 32 * x + 8 * t + 4 * e) =
-                    make_float4((o[x][0][e] + o[x][0][e + 2]) * f, (o[x][1][e] + o[x][1][e + 2]) * f,
-                                (o[x][2][e] + o[x][2][e + 2]) * f, (o[x][3][e] + o[x][3][e + 2]) * f);
+                    make_float4(o[x][0][e] * f, o[x][1][e] * f, o[x][2][e] * f, o[x][3][e] * f);
         if (part && t == 0) *reinterpret_cast<float2 *>(part + 8 * D + 2 * g) = make_float2(m, sum);
     }
 };

@@ -125,8 +125,8 @@ __global__ void __launch_bounds__(F32<D>::kThreads) attn_prefill_f32(const __gri
         __syncwarp();
         ok = __all_sync(0xffffffffu, ok && bar_wait(&full[kg][st], (it >> 1) & 1));
         if (!ok) break;
-        // rows g, g (tokens 2t, 2t + 1), g + 8, g + 8; the three products are
-        // summed apart, which keeps three chains of MMAs going per 8 keys
+        // rows g, g (tokens 2t, 2t + 1), g + 8, g + 8; the large products of
+        // the two K steps and the small ones are summed apart
         float s[NT][4], s1[NT][4], s2[NT][4];
 #pragma unroll
         for (int k = 0; k < NT; ++k)
@@ -147,8 +147,8 @@ __global__ void __launch_bounds__(F32<D>::kThreads) attn_prefill_f32(const __gri
                     split_tf32(*reinterpret_cast<const float4 *>(stage + x * T::kBoxBytes + (8 * k + g) * 128 + (((2 * t + j) ^ g) << 4)), kk);
 #pragma unroll
                     for (int h = 0; h < 8; h += 4) {
-                        mma_1688(s[k], qa[h], qb[h], qa[h + 2], qb[h + 2], kk[h], kk[h + 2]);
-                        mma_1688(s1[k], qa[h + 1], qb[h + 1], qa[h + 3], qb[h + 3], kk[h], kk[h + 2]);
+                        mma_1688(h ? s1[k] : s[k], qa[h], qb[h], qa[h + 2], qb[h + 2], kk[h], kk[h + 2]);
+                        mma_1688(s2[k], qa[h + 1], qb[h + 1], qa[h + 3], qb[h + 3], kk[h], kk[h + 2]);
                         mma_1688(s2[k], qa[h], qb[h], qa[h + 2], qb[h + 2], kk[h + 1], kk[h + 3]);
                     }
                 }
@@ -239,7 +239,12 @@ __global__ void __launch_bounds__(F32<D>::kThreads) attn_prefill_f32(const __gri
         // lane (g, t) reads chunk g of the rows of its two tokens: channel
         // 4 g + i of a box is column g of the box's MMA i
 #pragma unroll
-        for (int x = 0; x < NB; ++x)
+        for (int x = 0; x < NB; ++x) {
+            float c[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[i][e] = 0.0f;
 #pragma unroll
             for (int k = 0; k < NT; ++k) {
                 const unsigned char *vp = stage + T::kHalfBytes + x * T::kBoxBytes + (8 * k + 2 * t) * 128;
@@ -247,12 +252,17 @@ __global__ void __launch_bounds__(F32<D>::kThreads) attn_prefill_f32(const __gri
                 split_tf32(*reinterpret_cast<const float4 *>(vp + ((g ^ (2 * t)) << 4)), v0);
                 split_tf32(*reinterpret_cast<const float4 *>(vp + 128 + ((g ^ (2 * t + 1)) << 4)), v1);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mma_1688(o[x][i], w[k][0], w[k][4], w[k][2], w[k][6], v0[2 * i], v1[2 * i]);
+                for (int i = 0; i < 4; ++i) mma_1688(c[i], w[k][0], w[k][4], w[k][2], w[k][6], v0[2 * i], v1[2 * i]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mma_1688(o[x][i], w[k][1], w[k][5], w[k][3], w[k][7], v0[2 * i], v1[2 * i]);
+                for (int i = 0; i < 4; ++i) mma_1688(c[i], w[k][1], w[k][5], w[k][3], w[k][7], v0[2 * i], v1[2 * i]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mma_1688(o[x][i], w[k][0], w[k][4], w[k][2], w[k][6], v0[2 * i + 1], v1[2 * i + 1]);
+                for (int i = 0; i < 4; ++i) mma_1688(c[i], w[k][0], w[k][4], w[k][2], w[k][6], v0[2 * i + 1], v1[2 * i + 1]);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[x][i][e] += c[i][e];
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[kg][st]);
     }
@@ -316,7 +326,9 @@ cudaError_t launch_f32(const AttnArgs &a, cudaStream_t stream) {
     const int gs = group_shift_of(a);
     CUtensorMap km, vm;
     if (!page_map(&km, a.k_pages, D, a, false, 16) || !page_map(&vm, a.v_pages, D, a, false, 16)) return cudaErrorInvalidValue;
-    const unsigned grid = (unsigned)(query_tiles(a, T::kRows >> gs) * (a.Hq >> gs));
+    const long long blocks = query_tiles(a, T::kRows >> gs) * (a.Hq >> gs);
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)blocks;
     kern<<<grid, T::kThreads, T::kSmem, stream>>>(km, vm, a, gs);
     return cudaGetLastError();
 }
@@ -424,11 +436,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
         : "memory");
 }
 
-template <int D>
+// NS query tiles of 128 rows ("streams") to a block.
+template <int D, int NS>
 struct Tc {
-    static constexpr int kStreams = D == 256 ? 1 : 2;     // query tiles of 128 rows
+    static constexpr int kStreams = NS;
     static constexpr int kKeys = D == 128 ? 128 : 64;     // keys of a tile
-    static constexpr int kTiles = D == 128 ? 1 : 2;       // score tiles of a stream in TMEM
+    static constexpr int kTiles = D == 256 || NS == 2 && D == 64 ? 2 : 1;  // score tiles of a stream in TMEM
     static constexpr int kHalves = D / 64;                // 128-byte column blocks
     static constexpr int kQBytes = 128 * D * 2;           // a query tile
     static constexpr int kSlotBytes = kKeys * D * 2;      // a tile of K or V
@@ -446,17 +459,17 @@ struct Tc {
 };
 
 struct TcBars {
-    uint64_t q_full, kv_full[5], kv_empty[5], s_full[4], p_half[2], p_ready[2], o_done[2], tail;
+    uint64_t q_full, kv_full[5], kv_empty[5], s_full[4], p_half[4], p_ready[4], o_done[4], tail;
 };
 
 // One block: 128 kStreams rows, each a (token, head) pair of `group` heads
 // that share a key-value head (head fastest), against the tiles of keys.
-template <int D, bool CAP>
-__global__ void __launch_bounds__(Tc<D>::kThreads, 1)
+template <int D, int NS, bool CAP>
+__global__ void __launch_bounds__(Tc<D, NS>::kThreads, 1)
     attn_prefill_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap, const AttnArgs a, const int group_shift, const int box_shift) {
-    using T = Tc<D>;
-    constexpr int NS = T::kStreams, KT = T::kKeys, NH = T::kHalves;
+    using T = Tc<D, NS>;
+    constexpr int KT = T::kKeys, NH = T::kHalves;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *qs = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char *ring = qs + NS * T::kQBytes;
@@ -476,14 +489,14 @@ __global__ void __launch_bounds__(Tc<D>::kThreads, 1)
     const int h0 = at.head, kv = h0 / (a.Hq / a.Hkv);
     const int p0 = qt.start + qt.first, len = p0 + qt.rows;  // keys any row sees: lo .. len - 1
     const int lo = a.window > 0 && p0 + 1 > a.window ? p0 + 1 - a.window : 0;
-    // (a second stream without rows is left out)
-    const int streams = NS == 2 && qt.rows > tokens / 2 ? 2 : 1;
+    // (streams without rows are left out)
+    const int streams = (qt.rows * NS + tokens - 1) / tokens;
     const int k_first = lo / KT, n = (len - 1) / KT - k_first + 1;
 
     if (tid < (int)(sizeof(TcBars) / sizeof(uint64_t))) {
         // a thread per barrier (each initialisation ends in a fence)
         uint64_t *bar = reinterpret_cast<uint64_t *>(&bars) + tid;
-        mbar_init(bar, bar == &bars.p_half[0] || bar == &bars.p_half[1] || bar == &bars.p_ready[0] || bar == &bars.p_ready[1] ? 4 : 1);
+        mbar_init(bar, bar >= bars.p_half && bar < bars.o_done ? 4 : 1);  // (the weights' barriers: a warp each)
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -820,11 +833,11 @@ bool query_map(CUtensorMap *m, const AttnArgs &a, int D, int heads) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool CAP>
+template <int D, int NS, bool CAP>
 cudaError_t launch_tc(const AttnArgs &a, cudaStream_t stream) {
-    using T = Tc<D>;
+    using T = Tc<D, NS>;
     static std::atomic<uint64_t> ready{0};
-    auto kern = attn_prefill_tc<D, CAP>;
+    auto kern = attn_prefill_tc<D, NS, CAP>;
     const cudaError_t e = allow_smem(kern, ready, T::kSmem);
     if (e != cudaSuccess) return e;
     const int gs = group_shift_of(a);
@@ -834,14 +847,31 @@ cudaError_t launch_tc(const AttnArgs &a, cudaStream_t stream) {
     if (!query_map(&qm, a, D, 1 << gs) || !page_map(&km, a.k_pages, D, a, true, 1 << bs) ||
         !page_map(&vm, a.v_pages, D, a, true, 1 << bs))
         return cudaErrorInvalidValue;
-    const unsigned grid = (unsigned)(query_tiles(a, 128 * T::kStreams >> gs) * (a.Hq >> gs));
+    const long long blocks = query_tiles(a, 128 * NS >> gs) * (a.Hq >> gs);
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)blocks;
     kern<<<grid, T::kThreads, T::kSmem, stream>>>(qm, km, vm, a, gs, bs);
     return cudaGetLastError();
 }
 
+template <int D, int NS>
+cudaError_t launch_tc_ns(const AttnArgs &a, cudaStream_t stream) {
+    return a.softcap > 0.0f ? launch_tc<D, NS, true>(a, stream) : launch_tc<D, NS, false>(a, stream);
+}
+
 template <int D>
 cudaError_t launch_tc_d(const AttnArgs &a, cudaStream_t stream) {
-    return a.softcap > 0.0f ? launch_tc<D, true>(a, stream) : launch_tc<D, false>(a, stream);
+    if constexpr (D == 64) {
+        // four streams keep the softmax pipes busier (2 x 4096 tokens on a
+        // 4096-token prefix, 32 heads: 752 -> 688 us), where blocks of 512
+        // rows still come to a few per SM (2 x 512 tokens: 15 -> 23 us)
+        const int gs = group_shift_of(a);
+        int sms = 0;
+        const cudaError_t e = device_sms(&sms);
+        if (e != cudaSuccess) return e;
+        if (query_tiles(a, 512 >> gs) * (a.Hq >> gs) >= 3LL * sms) return launch_tc_ns<64, 4>(a, stream);
+    }
+    return launch_tc_ns<D, D == 256 ? 1 : 2>(a, stream);
 }
 
 }  // namespace

@@ -510,3 +510,28 @@ def test_hybrid_step_feeds_the_linear_attention_decode():
     # quotient lies within FP32 rounding of a tie: far fewer than 1 in 1000
     assert err < 2.0 ** -8
     no_device_errors()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,window,softcap,new,start", [
+    (64, 1, 64, 0, 0.0, [4001, 130], [5, 0]),
+    (64, 1, 64, 700, 20.0, [1500, 2600, 3], [0, 300, 64]),
+    (32, 4, 128, 0, 0.0, [1900], [400]),
+])
+def test_prefill_of_many_rows(Hq, Hkv, D, window, softcap, new, start):
+    """Long enough for blocks of the most rows (head size 64) and for several
+    waves of blocks."""
+    g = gen(Hq + D + window)
+    cfg = lq.AttnConfig(Hq, Hkv, D, window=window, softcap=softcap)
+    pg = Paged(g, cfg, len(new), 64, -(-max(n + s for n, s in zip(new, start)) // 64))
+    pg.fill(g, [n + s for n, s in zip(new, start)])
+    T = sum(new) + 2
+    cu = torch.tensor([0] + torch.tensor(new).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    q = randn(g, T, Hq, D, dtype=torch.bfloat16, scale=2.0)
+    o = torch.full((T, Hq, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    lq.lq_attn_prefill(cfg, pg.cache, torch.tensor(start, dtype=torch.int32, device="cuda"), cu, q, o)
+    row = 0
+    for b, (n, s) in enumerate(zip(new, start)):
+        check_attention(cfg, pg, q[row:row + n], o[row:row + n], b, s, 2.0 ** -8, f"sequence {b}")
+        row += n
+    assert (o[row:] == 3.0).all()
+    no_device_errors()
