@@ -430,9 +430,9 @@ typedef struct {
     int32_t window;    /* > 0: a query sees itself and the window - 1 tokens
                           before it; 0: all tokens before it                 */
     float eps;         /* > 0 and finite (used with a norm)                  */
-    float scale;       /* factor of q . k; finite                            */
-    float softcap;     /* > 0: scores s become softcap tanh(s / softcap)
-                          before the mask; 0: off                            */
+    float scale;       /* factor of q . k; |scale| <= 1e6                    */
+    float softcap;     /* in [1e-3, 1e6]: scores s become softcap
+                          tanh(s / softcap) before the mask; 0: off          */
 } lq_attn_config;
 
 /* A paged key-value cache: pages of page_size tokens, a page holding all

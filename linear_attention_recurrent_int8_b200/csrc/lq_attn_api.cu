@@ -28,8 +28,8 @@ lq_status check_config(const lq_attn_config *c) {
     if (c->rot_dim < 0 || c->rot_dim > c->head_dim || c->rot_dim % 16 != 0) return LQ_ERR_INVALID_ARGUMENT;
     if (c->rot_pairs != LQ_ROT_HALVES && c->rot_pairs != LQ_ROT_ADJACENT) return LQ_ERR_INVALID_ARGUMENT;
     if (c->window < 0) return LQ_ERR_INVALID_ARGUMENT;
-    if (!std::isfinite(c->scale) || !(c->softcap >= 0.0f && std::isfinite(c->softcap)))
-        return LQ_ERR_INVALID_ARGUMENT;
+    if (!(std::fabs(c->scale) <= 1e6f)) return LQ_ERR_INVALID_ARGUMENT;
+    if (c->softcap != 0.0f && !(c->softcap >= 1e-3f && c->softcap <= 1e6f)) return LQ_ERR_INVALID_ARGUMENT;
     return LQ_OK;
 }
 

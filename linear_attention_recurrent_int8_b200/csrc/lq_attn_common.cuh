@@ -161,22 +161,26 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
-// cap tanh(scale s / cap) in units of log2.  For BF16 outputs by
-// tanh y = 1 - 2 / (1 + e^{2y}), whose absolute error is a few FP32 steps of
-// cap: far below a BF16 step of any output.  FP32 outputs take tanhf.
+// cap tanh(scale s / cap) in units of log2.  FP32 outputs take tanhf.  For
+// BF16 ones tanh y = 1 - 2 / (1 + e^{2y}), and below 1/4, where the difference
+// loses digits that a large cap would bring back, the series to y^7.
 struct SoftCap {
-    float in, out;  // 2 log2(e) scale / cap (BF16) or scale / cap (FP32), and log2(e) cap
+    float in, out;  // scale / cap and log2(e) cap
 };
 
-template <bool BF16>
-__device__ __forceinline__ SoftCap soft_cap(float scale, float cap) {
-    return SoftCap{(BF16 ? 2.0f * kLog2e : 1.0f) * scale / cap, kLog2e * cap};
-}
+__device__ __forceinline__ SoftCap soft_cap(float scale, float cap) { return SoftCap{scale / cap, kLog2e * cap}; }
 
 template <bool BF16>
 __device__ __forceinline__ float capped_log2(float s, const SoftCap &c) {
-    if constexpr (BF16) return fmaf(-2.0f * c.out, rcp(1.0f + ex2(s * c.in)), c.out);
-    else return c.out * tanhf(s * c.in);
+    const float y = s * c.in;
+    if constexpr (BF16) {
+        const float u = y * y;
+        const float near = y * fmaf(u, fmaf(u, fmaf(u, -17.0f / 315.0f, 2.0f / 15.0f), -1.0f / 3.0f), 1.0f);
+        const float far = fmaf(-2.0f, rcp(1.0f + ex2(2.0f * kLog2e * y)), 1.0f);
+        return c.out * (fabsf(y) < 0.25f ? near : far);
+    } else {
+        return c.out * tanhf(y);
+    }
 }
 
 // Programmatic dependent launch: lets the next launch of the stream start,

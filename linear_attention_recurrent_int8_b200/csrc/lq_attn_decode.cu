@@ -184,7 +184,7 @@ struct Bf16Core {
             }
         }
         const bool part = tok0 + 16 > len || tok0 < lo;
-        const SoftCap cap = soft_cap<true>(a.scale, a.softcap);
+        const SoftCap cap = soft_cap(a.scale, a.softcap);
         float mx[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -412,7 +412,7 @@ struct F32Core {
             }
             __syncwarp();
         }
-        const SoftCap cap = soft_cap<false>(a.scale, a.softcap);
+        const SoftCap cap = soft_cap(a.scale, a.softcap);
         float mx = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NT; ++n)

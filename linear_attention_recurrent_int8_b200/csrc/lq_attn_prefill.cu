@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(F32<D>::kThreads) attn_prefill_f32(const __gri
     }
     __syncthreads();
 
-    const SoftCap cap = soft_cap<false>(a.scale, a.softcap);
+    const SoftCap cap = soft_cap(a.scale, a.softcap);
     int pos[2];  // of rows g and g + 8
     for (int r = 0; r < 2; ++r) pos[r] = p0 + ((16 * rg + g + 8 * r) >> group_shift);
     const int pw0 = p0 + ((16 * rg) >> group_shift), pw1 = p0 + ((16 * rg + 15) >> group_shift);
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, 1)
         // scores enter as 2^(c x): c = log2(e) |scale| (never 0, so that a
         // masked score stays -inf), or 1 for capped scores
         const float c = CAP ? 1.0f : fmaxf(fabsf(a.scale * kLog2e), 1e-30f);
-        const SoftCap cap = soft_cap<true>(a.scale, a.softcap);
+        const SoftCap cap = soft_cap(a.scale, a.softcap);
         const CapPoly poly = cap_poly(a.scale / a.softcap, cap.out);
         const float in_reach = kTanhReach * a.softcap / fabsf(a.scale);
         float m = -INFINITY, l = 0.0f;

@@ -276,3 +276,10 @@ def test_reference_rotation_by_hand():
     assert torch.allclose(y[0, 0, :2], torch.tensor([-0.8, 0.6], dtype=torch.float64))
     y, _ = ref.norm_rotate(x, 0, 0.0, None, 16, False, cs, torch.tensor([1]))
     assert y[0, 0, 8] == 3.0 and y[0, 0, 9] == 4.0 and y[0, 0, 0] == 0.0
+
+
+@pytest.mark.parametrize("change", [dict(softcap=1e-4), dict(softcap=2e6), dict(softcap=float("inf")), dict(scale=-2e6),
+                                    dict(scale=float("nan"))])
+def test_scales_and_caps_out_of_range_are_refused(change):
+    assert decode_call(cfg_c(**change), cache_c()) == INVALID
+    assert prefill_call(cfg_c(**change), cache_c()) == INVALID

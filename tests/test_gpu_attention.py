@@ -535,3 +535,24 @@ def test_prefill_of_many_rows(Hq, Hkv, D, window, softcap, new, start):
         row += n
     assert (o[row:] == 3.0).all()
     no_device_errors()
+
+
+@pytest.mark.parametrize("io,split", [(BF, 2.0 ** -17), (F32, 0.0)])
+@pytest.mark.parametrize("scale,softcap", [(0.3, 1e4), (0.3, 1.0), (-0.2, 10.0), (0.0, 0.0), (-0.1, 0.0), (3.0, 300.0)])
+def test_scales_and_caps(io, split, scale, softcap):
+    """Caps far above and well below the scores, scales of either sign and zero."""
+    g = gen(int(1000 * scale) % 97 + int(softcap))
+    cfg = lq.AttnConfig(4, 2, 64, io_dtype=io, scale=scale, softcap=softcap)
+    n = 150
+    pg = Paged(g, cfg, 2, 16, 10)
+    pg.fill(g, [n, n])
+    q = randn(g, 40, 4, 64, dtype=DT[io], scale=2.0)
+    o = torch.empty_like(q)
+    lq.lq_attn_prefill(cfg, pg.cache, torch.full((2,), n - 20, dtype=torch.int32, device="cuda"), None, q, o)
+    for b in range(2):
+        check_attention(cfg, pg, q[20 * b:20 * b + 20], o[20 * b:20 * b + 20], b, n - 20, 2.0 ** -8 if io == BF else 0.0, "prefill")
+    qd, od = q[:2].contiguous(), torch.empty(2, 4, 64, dtype=DT[io], device="cuda")
+    lq.lq_attn_decode(cfg, pg.cache, torch.full((2,), n - 1, dtype=torch.int32, device="cuda"), qd, od)
+    for b in range(2):
+        check_attention(cfg, pg, qd[b:b + 1], od[b:b + 1], b, n - 1, split, "decode")
+    no_device_errors()
