@@ -429,7 +429,7 @@ typedef struct {
     int32_t rot_pairs; /* lq_rot_pairs                                       */
     int32_t window;    /* > 0: a query sees itself and the window - 1 tokens
                           before it; 0: all tokens before it                 */
-    float eps;         /* > 0 and finite (used with a norm)                  */
+    float eps;         /* >= 1e-30 and finite (used with a norm)             */
     float scale;       /* factor of q . k; |scale| <= 1e6                    */
     float softcap;     /* in [1e-3, 1e6]: scores s become softcap
                           tanh(s / softcap) before the mask; 0: off          */
@@ -522,7 +522,11 @@ LQ_API int64_t lq_attn_workspace_bytes(const lq_attn_config *cfg, int32_t batch)
  * and recorded (LQ_DEVERR_BAD_PAGE): that sequence's output is not valid.
  * The tokens of all sequences are shared out evenly over the GPU and the
  * parts of a sequence joined in a fixed order: results do not depend on
- * scheduling.  Two launches. */
+ * scheduling.  (The split, and with it the rounding, depends on the lengths
+ * of all sequences of the call.)  An infinite value v that is visible makes
+ * its channel of the output infinite or NaN.  Two launches.
+ * LQ_ERR_UNSUPPORTED where batch * max_pages * page_size reaches 2^34, or
+ * that times Hq 2^40. */
 LQ_API lq_status lq_attn_decode(const lq_attn_config *cfg, const lq_kv_cache *cache,
                                 const int32_t *pos, const void *q, void *o, void *workspace,
                                 size_t workspace_bytes, lq_stream_t stream);
@@ -535,7 +539,11 @@ LQ_API lq_status lq_attn_decode(const lq_attn_config *cfg, const lq_kv_cache *ca
  * with a position >= max_pages * page_size leaves its row as it is
  * (LQ_DEVERR_BAD_POSITION); bad pages as for lq_attn_decode.  tokens == 0 is
  * a no-op.  One launch.  With io_dtype LQ_BF16 the softmax weights are
- * rounded to BF16 for the product with V. */
+ * rounded to BF16 for the product with V.
+ * Places of the cache that no new token of a sequence sees may hold anything,
+ * NaN included.  A NaN or infinite value v that some of a sequence's new
+ * tokens see may also reach outputs of its others (their weight for it is
+ * zero, and zero times infinity is not). */
 LQ_API lq_status lq_attn_prefill(const lq_attn_config *cfg, const lq_kv_cache *cache,
                                  const int32_t *pos, const int32_t *cu_tokens, int32_t tokens,
                                  const void *q, void *o, lq_stream_t stream);

@@ -24,7 +24,7 @@ lq_status check_config(const lq_attn_config *c) {
     if (c->io_dtype != LQ_F32 && c->io_dtype != LQ_BF16) return LQ_ERR_INVALID_ARGUMENT;
     if (c->norm != LQ_NORM_NONE && c->norm != LQ_NORM_L2 && c->norm != LQ_NORM_RMS)
         return LQ_ERR_INVALID_ARGUMENT;
-    if (c->norm != LQ_NORM_NONE && !(c->eps > 0.0f && std::isfinite(c->eps))) return LQ_ERR_INVALID_ARGUMENT;
+    if (c->norm != LQ_NORM_NONE && !(c->eps >= 1e-30f && std::isfinite(c->eps))) return LQ_ERR_INVALID_ARGUMENT;
     if (c->rot_dim < 0 || c->rot_dim > c->head_dim || c->rot_dim % 16 != 0) return LQ_ERR_INVALID_ARGUMENT;
     if (c->rot_pairs != LQ_ROT_HALVES && c->rot_pairs != LQ_ROT_ADJACENT) return LQ_ERR_INVALID_ARGUMENT;
     if (c->window < 0) return LQ_ERR_INVALID_ARGUMENT;

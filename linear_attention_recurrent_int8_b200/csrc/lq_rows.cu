@@ -92,6 +92,13 @@ __device__ __forceinline__ void load4(float *v, const float *p) {
     v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
 }
 
+// 1 / sqrt(x) of a normal x, to 2^-22.9.
+__device__ __forceinline__ float rsqrt_normal(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // One block: NR rows for each of its groups of D / 8 lanes, all of token
 // blockIdx.x; rows are the q heads, the k heads and, when appending, the v
 // heads (copied).  SPLIT (rotation by halves): the lanes of the rotated
@@ -190,7 +197,7 @@ __global__ void __launch_bounds__(256, NR == 4 ? 4 : 6) rows_kernel(const RowsAr
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
             ss = group_sum<L>(ss);
-            const float f = rsqrtf(a.norm == 2 ? fmaf(ss, 1.0f / D, a.eps) : ss + a.eps);
+            const float f = rsqrt_normal(a.norm == 2 ? fmaf(ss, 1.0f / D, a.eps) : ss + a.eps);
             const float *w = r < a.Hq ? a.q_weight : a.k_weight;
             if (w) {
                 float wv[8];

@@ -283,3 +283,8 @@ def test_reference_rotation_by_hand():
 def test_scales_and_caps_out_of_range_are_refused(change):
     assert decode_call(cfg_c(**change), cache_c()) == INVALID
     assert prefill_call(cfg_c(**change), cache_c()) == INVALID
+
+
+def test_the_smallest_eps():
+    assert norm_call(cfg_c(norm=lq.LQ_NORM_L2, eps=1e-31)) == INVALID
+    assert norm_call(cfg_c(norm=lq.LQ_NORM_L2, eps=1e-30), tokens=0) == OK

@@ -556,3 +556,47 @@ def test_scales_and_caps(io, split, scale, softcap):
     for b in range(2):
         check_attention(cfg, pg, qd[b:b + 1], od[b:b + 1], b, n - 1, split, "decode")
     no_device_errors()
+
+
+LONG_APPEND_CASES = [
+    # as APPEND_CASES, over many blocks
+    ([2000, 0, 1, 900, 700, 0, 1500], [0, 3, 60, -1, 7, 0, 1000], 16, 2, 256, 16, lq.LQ_NORM_RMS, 64, lq.LQ_ROT_HALVES, BF),
+    ([800, 800, 800, 800], [5, -1, 0, 255], 32, 8, 128, 64, lq.LQ_NORM_L2, 128, lq.LQ_ROT_ADJACENT, BF),
+    ([1300, 17, 2100], [100, 0, 31], 8, 4, 128, 32, lq.LQ_NORM_RMS, 48, lq.LQ_ROT_HALVES, F32),
+    ([5000, 0, 4000], [0, 9, 300], 24, 8, 64, 256, lq.LQ_NORM_NONE, 0, 0, BF),
+    ([1, 3000, 1], [8, 0, 8], 20, 5, 256, 128, lq.LQ_NORM_NONE, 256, lq.LQ_ROT_HALVES, F32),
+]
+
+
+@pytest.mark.parametrize("new,start,Hq,Hkv,D,page,norm,rot,pairs,io", LONG_APPEND_CASES)
+@pytest.mark.parametrize("with_q", [True, False])
+def test_long_append(new, start, Hq, Hkv, D, page, norm, rot, pairs, io, with_q):
+    test_append(new, start, Hq, Hkv, D, page, norm, rot, pairs, io, with_q)
+
+
+def test_long_norm_with_padding_positions_and_in_place():
+    """Adjacent and split rotation over many tokens, q alone and in place."""
+    for pairs, rot, io in ((lq.LQ_ROT_ADJACENT, 64, BF), (lq.LQ_ROT_HALVES, 128, F32)):
+        test_norm_rotate(6001, 32, 8, 128, lq.LQ_NORM_RMS, True, rot, pairs, io)
+
+
+def test_long_append_reports_bad_places():
+    g = gen(10)
+    cfg = lq.AttnConfig(32, 8, 128, rot_dim=128)
+    B, n, page = 4, 1000, 64
+    pg = Paged(g, cfg, B, page, 17)
+    pg.table[1, 3] = pg.k.shape[0]   # tokens 192 .. 255 of sequence 1 have no page
+    pg.table[2, 15] = -1             # tokens 960 .. of sequence 2
+    k = randn(g, B * n, 8, 128, dtype=torch.bfloat16)
+    q = randn(g, B * n, 32, 128, dtype=torch.bfloat16)
+    qo = torch.full_like(q, 3.0)
+    cs = ref.table(128, 1080).cuda()
+    pos = torch.tensor([0, 0, 0, 100], dtype=torch.int32, device="cuda")  # the last 12 + 8 rows of sequence 3: past table and cache
+    lq.lq_kv_append(cfg, pg.cache, pos, None, q, k, k, None, None, cs, qo)
+    assert lq.lq_device_errors() == lq.LQ_DEVERR_BAD_PAGE | lq.LQ_DEVERR_BAD_POSITION
+    gone = torch.zeros(B * n, dtype=torch.bool)
+    gone[n + 192:n + 256] = True
+    gone[2 * n + 960:3 * n] = True
+    gone[3 * n + 980:] = True
+    assert (qo[gone.cuda()] == 3.0).all() and (qo[~gone.cuda()] != 3.0).any(-1).any(-1).all()
+    assert int((~pg.v.isnan()).sum()) == int((~gone).sum()) * 8 * 128
