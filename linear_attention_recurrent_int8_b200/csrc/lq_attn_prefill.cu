@@ -43,11 +43,11 @@ struct F32 {
 // One block: 32 rows, each a (token, head) pair of heads that share a
 // key-value head (head fastest).  Warp w takes 16 rows (w % 2) and every
 // second tile of keys (w / 2), and the two halves of a row's keys are joined
-// at the end.  The two warps of a tile share the buffers for K and V: K of a
-// coming tile comes in while the weights meet V, V while the queries meet K
-// (at head size 256 one buffer each leaves room for a second block on the SM:
-// 6.6 -> 4.9 ms for 2 x 2048 tokens on a prefix).  Products of two-part
-// operands: hi hi + hi lo + lo hi, 3 MMAs.
+// at the end.  The two warps of a tile share two buffers of K and V; at head
+// size 256 there is one, of which K's part is filled again while the weights
+// meet V and V's part while the queries meet K: that leaves room for a second
+// block on the SM (6.6 -> 4.9 ms for 2 x 2048 tokens on a prefix).  Products
+// of two-part operands: hi hi + hi lo + lo hi, 3 MMAs.
 template <int D>
 __global__ void __launch_bounds__(F32<D>::kThreads, D == 64 ? 3 : 2) attn_prefill_f32(const __grid_constant__ CUtensorMap kmap,
                                                                      const __grid_constant__ CUtensorMap vmap,
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(F32<D>::kThreads, D == 64 ? 3 : 2) attn_prefil
     extern __shared__ unsigned char smem_raw[];
     unsigned char *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     float *qs = reinterpret_cast<float *>(ring + 4 * NBUF * T::kHalfBytes);
-    __shared__ uint64_t full[2][2][2], empty[2][2][2];  // [key group][K, V][buffer]
+    __shared__ uint64_t full[2][2][2], empty[2][2][2];  // [key group][K (and V with two buffers), V][buffer]
     __shared__ int find[T::kThreads / 32 + 6];
     const BlockPlace at = place_of(a, group_shift);
     const QueryTile qt = find_query_tile<T::kThreads>(a, T::kRows >> group_shift, at.tile, find);
@@ -71,12 +71,13 @@ __global__ void __launch_bounds__(F32<D>::kThreads, D == 64 ? 3 : 2) attn_prefil
 
     if (tid < 8) mbar_init(&full[0][0][0] + tid, 1), mbar_init(&empty[0][0][0] + tid, 2);
     __syncthreads();
-    // one lane of a key group fills its buffers: K (0) or V (1) of its i-th tile
+    // One lane of a key group fills its buffers for the group's i-th tile: K
+    // (v = 0) or V (1) where the group has one buffer of each, else both.
     auto issue = [&](int i, int v) {
         const int k0 = (k_first + 2 * i + kg) * KT;
         uint64_t *bar = &full[kg][v][i % NBUF];
-        unsigned char *dst = ring + ((2 * kg + v) * NBUF + i % NBUF) * T::kHalfBytes;
-        mbar_arrive_expect_tx(bar, T::kHalfBytes);
+        unsigned char *kdst = ring + (2 * kg * NBUF + i % NBUF) * T::kHalfBytes, *vdst = kdst + NBUF * T::kHalfBytes;
+        mbar_arrive_expect_tx(bar, NBUF > 1 ? 2 * T::kHalfBytes : T::kHalfBytes);
         for (int r = 0; r < KT; r += 16) {
             const int tok = k0 + r;
             int z = -1;  // rows past the visible keys are filled with zeros
@@ -85,13 +86,19 @@ __global__ void __launch_bounds__(F32<D>::kThreads, D == 64 ? 3 : 2) attn_prefil
                 if (page >= 0 && page < a.num_pages) z = page * a.Hkv + kv;
                 else atomicOr(&g_dev_error, kErrBadPage);
             }
-            for (int x = 0; x < NB; ++x)
-                tma_page_load(dst + x * T::kBoxBytes + r * 128, v ? &vmap : &kmap, 32 * x, tok & (a.page_size - 1), z, bar);
+            for (int x = 0; x < NB; ++x) {
+                const int off = x * T::kBoxBytes + r * 128;
+                if (NBUF > 1 || v == 0) tma_page_load(kdst + off, &kmap, 32 * x, tok & (a.page_size - 1), z, bar);
+                if (NBUF > 1 || v == 1) tma_page_load(vdst + off, &vmap, 32 * x, tok & (a.page_size - 1), z, bar);
+            }
         }
     };
     const int mine = kg < n ? (n - kg + 1) / 2 : 0;  // tiles of the group
     const bool producer = rg == 0 && lane == 0;
-    for (int i = 0; producer && i < NBUF && i < mine; ++i) issue(i, 0), issue(i, 1);
+    for (int i = 0; producer && i < NBUF && i < mine; ++i) {
+        issue(i, 0);
+        if (NBUF == 1) issue(i, 1);
+    }
     for (int i = tid; i < T::kRows * (D / 4); i += T::kThreads) {
         const int r = i / (D / 4), c = 4 * (i % (D / 4)), tok = r >> group_shift;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -120,15 +127,11 @@ __global__ void __launch_bounds__(F32<D>::kThreads, D == 64 ? 3 : 2) attn_prefil
         const int buf = it % NBUF, phase = it / NBUF & 1;
         const unsigned char *kbuf = ring + (2 * kg * NBUF + buf) * T::kHalfBytes;
         unsigned char *vbuf = ring + ((2 * kg + 1) * NBUF + buf) * T::kHalfBytes;
-        // into the last tile's buffers, once both warps have left them
+        // into the last tile's buffer, once both warps have left it
         if (it > 0 && it - 1 + NBUF < mine && producer) {
             const int last = (it - 1) % NBUF, left = (it - 1) / NBUF & 1;
-            if (NBUF > 1) {
-                ok = bar_wait(&empty[kg][0][last], left);
-                if (ok) issue(it - 1 + NBUF, 0);
-            }
-            ok = ok && bar_wait(&empty[kg][1][last], left);
-            if (ok) issue(it - 1 + NBUF, 1);
+            ok = bar_wait(&empty[kg][1][last], left);
+            if (ok) issue(it - 1 + NBUF, NBUF == 1);
         }
         __syncwarp();
         ok = __all_sync(0xffffffffu, ok && bar_wait(&full[kg][0][buf], phase));
@@ -193,9 +196,9 @@ __global__ void __launch_bounds__(F32<D>::kThreads, D == 64 ? 3 : 2) attn_prefil
                         if (4 * k + e == i) s[k][e] = v;
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[kg][0][buf]);
         if constexpr (NBUF == 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[kg][0][0]);
             // the next K at once
             if (it + 1 < mine && producer) {
                 ok = bar_wait(&empty[kg][0][0], phase);
@@ -242,8 +245,10 @@ __global__ void __launch_bounds__(F32<D>::kThreads, D == 64 ? 3 : 2) attn_prefil
                 l[e >> 1] += v;
                 split_tf32(v, w[k][2 * e], w[k][2 * e + 1]);
             }
-        ok = __all_sync(0xffffffffu, ok && bar_wait(&full[kg][1][buf], phase));
-        if (!ok) break;
+        if constexpr (NBUF == 1) {
+            ok = __all_sync(0xffffffffu, ok && bar_wait(&full[kg][1][0], phase));
+            if (!ok) break;
+        }
         if (k0 < lo || k0 + KT > len) {
             // rows of V that no row sees may hold NaN: weight 0 would not
             // silence them (either warp of the tile clears them all)
