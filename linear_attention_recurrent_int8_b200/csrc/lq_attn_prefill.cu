@@ -361,7 +361,7 @@ cudaError_t launch_f32(const AttnArgs &a, cudaStream_t stream) {
 // BF16: tensor cores
 // ---------------------------------------------------------------------------
 
-// A row of 128 or 64 consecutive TMEM columns for each of the warp's 32 lanes;
+// A row of 128, 64 or 16 consecutive TMEM columns for each of the warp's 32 lanes;
 // the wait is part of the statement.
 __device__ __forceinline__ void tmem_load_row(uint32_t taddr, float (&v)[128]) {
     uint32_t r[128];
@@ -383,6 +383,19 @@ __device__ __forceinline__ void tmem_store_row(uint32_t taddr, const float (&v)[
         "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
         "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_load_row(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "{ tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned; }"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // Maximum of three that keeps NaN.
@@ -465,7 +478,7 @@ template <int D, int NS>
 struct Tc {
     static constexpr int kStreams = NS;
     static constexpr int kKeys = D == 128 ? 128 : 64;     // keys of a tile
-    static constexpr int kTiles = D == 256 || NS == 2 && D == 64 ? 2 : 1;  // score tiles of a stream in TMEM
+    static constexpr int kTiles = D == 256 ? 2 : 1;  // score tiles of a stream in TMEM
     static constexpr int kHalves = D / 64;                // 128-byte column blocks
     static constexpr int kQBytes = 128 * D * 2;           // a query tile
     static constexpr int kSlotBytes = kKeys * D * 2;      // a tile of K or V
@@ -474,22 +487,24 @@ struct Tc {
     static constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
     static constexpr int kThreads = (kSoftWarps + 2) * 32;
     static constexpr int kSmem = 1024 + kStreams * kQBytes + kSlots * kSlotBytes;
-    // of 8 pairs of weights, those exponentiated on the FMA pipe
-    static constexpr int kFmaOf8 = 1;
     // TMEM columns: the score tiles, whose first half the weights overwrite,
     // then the outputs
-    static constexpr uint32_t kColS = 0, kColO = 256;
-    static constexpr uint32_t kCols = 512;
+    static constexpr uint32_t kColS = 0, kColO = kStreams * kTiles * kKeys;
+    static constexpr uint32_t kCols = kColO + NS * D <= 256 ? 256 : 512;
+    // At head size 64 half of TMEM is enough for a block, and a second block
+    // on the SM keeps its softmax pipes busy (2 x 4096 tokens on a 4096-token
+    // prefix, 32 heads: 752 -> 504 us; one block of four streams: 688).
+    static constexpr int kBlocks = 512 / kCols;
 };
 
 struct TcBars {
-    uint64_t q_full, kv_full[5], kv_empty[5], s_full[4], p_half[4], p_ready[4], o_done[4], tail;
+    uint64_t q_full, kv_full[5], kv_empty[5], s_full[2], p_half[2], p_ready[2], o_done[2], tail;
 };
 
 // One block: 128 kStreams rows, each a (token, head) pair of `group` heads
 // that share a key-value head (head fastest), against the tiles of keys.
 template <int D, int NS, bool CAP>
-__global__ void __launch_bounds__(Tc<D, NS>::kThreads, 1)
+__global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
     attn_prefill_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap, const AttnArgs a, const int group_shift, const int box_shift) {
     using T = Tc<D, NS>;
@@ -768,12 +783,12 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, 1)
                         tc_fence_after_sync();
                     }
 #pragma unroll 1
-                    for (int k = 0; k < D; k += 32) {
-                        float o[32];
-                        tmem_load32(oa + k, o);
+                    for (int k = 0; k < D; k += 16) {
+                        float o[16];
+                        tmem_load_row(oa + k, o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] *= f;
-                        tmem_store32(oa + k, o);
+                        for (int i = 0; i < 16; ++i) o[i] *= f;
+                        tmem_store_row(oa + k, o);
                     }
                 }
             }
@@ -786,13 +801,15 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, 1)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 constexpr int HW = KT / 4;  // words of half a tile's weights
+                // of 8 pairs of weights, those exponentiated on the FMA pipe
+                constexpr int kFmaOf8 = CAP ? 0 : 1;
                 float w[HW];
 #pragma unroll
                 for (int i = 0; i < HW; ++i) {
                     const int k = half * (KT / 2) + 2 * i;
                     const f32x2 v = fma2(two(x[k], x[k + 1]), c2, base2);
                     float e0, e1;
-                    if (i % 8 < T::kFmaOf8) {
+                    if (i % 8 < kFmaOf8) {
                         ex2_fma(v, e0, e1);
                     } else {
                         apart(v, e0, e1);
@@ -878,24 +895,10 @@ cudaError_t launch_tc(const AttnArgs &a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-template <int D, int NS>
-cudaError_t launch_tc_ns(const AttnArgs &a, cudaStream_t stream) {
-    return a.softcap > 0.0f ? launch_tc<D, NS, true>(a, stream) : launch_tc<D, NS, false>(a, stream);
-}
-
 template <int D>
 cudaError_t launch_tc_d(const AttnArgs &a, cudaStream_t stream) {
-    if constexpr (D == 64) {
-        // four streams keep the softmax pipes busier (2 x 4096 tokens on a
-        // 4096-token prefix, 32 heads: 752 -> 688 us), where blocks of 512
-        // rows still come to a few per SM (2 x 512 tokens: 15 -> 23 us)
-        const int gs = group_shift_of(a);
-        int sms = 0;
-        const cudaError_t e = device_sms(&sms);
-        if (e != cudaSuccess) return e;
-        if (query_tiles(a, 512 >> gs) * (a.Hq >> gs) >= 3LL * sms) return launch_tc_ns<64, 4>(a, stream);
-    }
-    return launch_tc_ns<D, D == 256 ? 1 : 2>(a, stream);
+    constexpr int NS = D == 256 ? 1 : 2;
+    return a.softcap > 0.0f ? launch_tc<D, NS, true>(a, stream) : launch_tc<D, NS, false>(a, stream);
 }
 
 }  // namespace
