@@ -6,6 +6,8 @@
 // pack the query heads that share a key-value head into the rows of a tile
 // (head fastest), so that a tile spans few tokens: its causal edge is short
 // and its keys are read once for all of its heads.
+#include <algorithm>
+
 #include "lq_attn_common.cuh"
 #include "lq_tc.cuh"
 
@@ -28,53 +30,55 @@ __device__ __forceinline__ BlockPlace place_of(const AttnArgs &a, int group_shif
 // FP32: warp MMAs on operands in two TF32 parts
 // ---------------------------------------------------------------------------
 
-template <int D>
+template <int D, int KG>
 struct F32 {
-    static constexpr int kRows = 32, kThreads = 128;
+    static constexpr int kThreads = 128;
+    static constexpr int kRowGroups = 4 / KG, kRows = 16 * kRowGroups;  // of 16 rows
     static constexpr int kKeys = D == 64 ? 32 : 16;         // keys of a tile
     static constexpr int kBoxes = D / 32;                   // 128-byte column blocks
     static constexpr int kBoxBytes = kKeys * 128;
     static constexpr int kHalfBytes = kBoxes * kBoxBytes;   // K of a tile, then V
     static constexpr int kLd = D + 4;                       // row stride of Q: rows on distinct banks
-    static constexpr int kBufs = D < 256 ? 2 : 1;           // tiles of K, and of V, that a key group holds
-    static constexpr int kSmem = 1024 + 4 * kBufs * kHalfBytes + kRows * kLd * 4;
+    static constexpr int kBufs = D < 256 && KG == 2 ? 2 : 1;         // tiles of K, and of V, that a key group holds
+    static constexpr int kSmem = 1024 + 2 * KG * kBufs * kHalfBytes + kRows * kLd * 4;
+    static constexpr int kBlocks = D == 64 ? 3 : D == 256 && KG == 4 ? 1 : 2;  // on an SM
 };
 
-// One block: 32 rows, each a (token, head) pair of heads that share a
-// key-value head (head fastest).  Warp w takes 16 rows (w % 2) and every
-// second tile of keys (w / 2), and the two halves of a row's keys are joined
-// at the end.  The two warps of a tile share two buffers of K and V; at head
-// size 256 there is one, of which K's part is filled again while the weights
-// meet V and V's part while the queries meet K: that leaves room for a second
-// block on the SM (6.6 -> 4.9 ms for 2 x 2048 tokens on a prefix).  Products
-// of two-part operands: hi hi + hi lo + lo hi, 3 MMAs.
-template <int D>
-__global__ void __launch_bounds__(F32<D>::kThreads, D == 64 ? 3 : 2) attn_prefill_f32(const __grid_constant__ CUtensorMap kmap,
-                                                                     const __grid_constant__ CUtensorMap vmap,
-                                                                     const AttnArgs a, const int group_shift) {
-    using T = F32<D>;
-    constexpr int KT = T::kKeys, NB = T::kBoxes, NT = KT / 8, LD = T::kLd, NBUF = T::kBufs;
+// One block: 16 or 32 rows, each a (token, head) pair of heads that share a
+// key-value head (head fastest).  A warp takes 16 rows and every KG-th tile of
+// keys, and the KG parts of a row's keys are joined at the end.  The warps of
+// a key group share two buffers of K and V, or one, of which K's part is
+// filled again while the weights meet V and V's part while the queries meet
+// K: that leaves room for a second block on the SM (head size 256, 2 x 2048
+// tokens on a prefix: 6.6 -> 4.9 ms).  Products of two-part operands:
+// hi hi + hi lo + lo hi, 3 MMAs.
+template <int D, int KG>
+__global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
+    attn_prefill_f32(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                     const AttnArgs a, const int group_shift) {
+    using T = F32<D, KG>;
+    constexpr int RG = T::kRowGroups, KT = T::kKeys, NB = T::kBoxes, NT = KT / 8, LD = T::kLd, NBUF = T::kBufs;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    float *qs = reinterpret_cast<float *>(ring + 4 * NBUF * T::kHalfBytes);
-    __shared__ uint64_t full[2][2][2], empty[2][2][2];  // [key group][K (and V with two buffers), V][buffer]
+    float *qs = reinterpret_cast<float *>(ring + 2 * KG * NBUF * T::kHalfBytes);
+    __shared__ uint64_t full[KG][2][2], empty[KG][2][2];  // [key group][K (and V with two buffers), V][buffer]
     __shared__ int find[T::kThreads / 32 + 6];
     const BlockPlace at = place_of(a, group_shift);
     const QueryTile qt = find_query_tile<T::kThreads>(a, T::kRows >> group_shift, at.tile, find);
     if (qt.rows <= 0) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int rg = warp & 1, kg = warp >> 1;
+    const int rg = warp % RG, kg = warp / RG;
     const int heads = 1 << group_shift, h0 = at.head, kv = h0 / (a.Hq / a.Hkv);
     const int p0 = qt.start + qt.first, len = p0 + qt.rows;  // keys any row sees: lo .. len - 1
     const int lo = a.window > 0 && p0 + 1 > a.window ? p0 + 1 - a.window : 0;
     const int k_first = lo / KT, n = (len - 1) / KT - k_first + 1;
 
-    if (tid < 8) mbar_init(&full[0][0][0] + tid, 1), mbar_init(&empty[0][0][0] + tid, 2);
+    if (tid < 4 * KG) mbar_init(&full[0][0][0] + tid, 1), mbar_init(&empty[0][0][0] + tid, RG);
     __syncthreads();
     // One lane of a key group fills its buffers for the group's i-th tile: K
     // (v = 0) or V (1) where the group has one buffer of each, else both.
     auto issue = [&](int i, int v) {
-        const int k0 = (k_first + 2 * i + kg) * KT;
+        const int k0 = (k_first + KG * i + kg) * KT;
         uint64_t *bar = &full[kg][v][i % NBUF];
         unsigned char *kdst = ring + (2 * kg * NBUF + i % NBUF) * T::kHalfBytes, *vdst = kdst + NBUF * T::kHalfBytes;
         mbar_arrive_expect_tx(bar, NBUF > 1 ? 2 * T::kHalfBytes : T::kHalfBytes);
@@ -93,7 +97,7 @@ __global__ void __launch_bounds__(F32<D>::kThreads, D == 64 ? 3 : 2) attn_prefil
             }
         }
     };
-    const int mine = kg < n ? (n - kg + 1) / 2 : 0;  // tiles of the group
+    const int mine = kg < n ? (n - kg + KG - 1) / KG : 0;  // tiles of the group
     const bool producer = rg == 0 && lane == 0;
     for (int i = 0; producer && i < NBUF && i < mine; ++i) {
         issue(i, 0);
@@ -123,7 +127,7 @@ __global__ void __launch_bounds__(F32<D>::kThreads, D == 64 ? 3 : 2) attn_prefil
             for (int e = 0; e < 4; ++e) o[x][i][e] = 0.0f;
     bool ok = true;
     for (int it = 0; it < mine; ++it) {
-        const int k0 = (k_first + 2 * it + kg) * KT;
+        const int k0 = (k_first + KG * it + kg) * KT;
         const int buf = it % NBUF, phase = it / NBUF & 1;
         const unsigned char *kbuf = ring + (2 * kg * NBUF + buf) * T::kHalfBytes;
         unsigned char *vbuf = ring + ((2 * kg + 1) * NBUF + buf) * T::kHalfBytes;
@@ -297,11 +301,12 @@ __global__ void __launch_bounds__(F32<D>::kThreads, D == 64 ? 3 : 2) attn_prefil
     }
     // join the two halves of the keys: group 1 hands over through shared memory
     __syncthreads();
-    float *jo = reinterpret_cast<float *>(ring) + rg * 16 * (D + 2);
-    if (kg == 1) {
+    constexpr int JLD = D + 2;
+    float *jo = reinterpret_cast<float *>(ring) + rg * 16 * JLD;
+    if (kg > 0) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            float *row = jo + (g + 8 * r) * (D + 2);
+            float *row = jo + (kg - 1) * T::kRows * JLD + (g + 8 * r) * JLD;
 #pragma unroll
             for (int x = 0; x < NB; ++x)
 #pragma unroll
@@ -312,14 +317,24 @@ __global__ void __launch_bounds__(F32<D>::kThreads, D == 64 ? 3 : 2) attn_prefil
         }
     }
     __syncthreads();
-    if (kg == 1 || !ok) return;
+    if (kg > 0 || !ok) return;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const int R = 16 * rg + g + 8 * r, tok = R >> group_shift;
         if (tok >= qt.rows) continue;
-        const float *row = jo + (g + 8 * r) * (D + 2);
-        const float m1 = row[D], top = fmaxf(m[r], m1), base = top == -INFINITY ? 0.0f : top;
-        const float f0 = ex2(m[r] - base), f1 = ex2(m1 - base), f = 1.0f / (l[r] * f0 + row[D + 1] * f1);
+        const float *row = jo + (g + 8 * r) * JLD;
+        float top = m[r], f[KG];
+#pragma unroll
+        for (int k = 1; k < KG; ++k) top = fmaxf(top, row[(k - 1) * T::kRows * JLD + D]);
+        const float base = top == -INFINITY ? 0.0f : top;
+        f[0] = ex2(m[r] - base);
+        float sum = l[r] * f[0];
+#pragma unroll
+        for (int k = 1; k < KG; ++k) {
+            f[k] = ex2(row[(k - 1) * T::kRows * JLD + D] - base);
+            sum += row[(k - 1) * T::kRows * JLD + D + 1] * f[k];
+        }
+        const float inv = 1.0f / sum;
         float *dst = static_cast<float *>(a.o) + ((size_t)(qt.base + qt.first + tok) * a.Hq + h0 + (R & (heads - 1))) * D;
 #pragma unroll
         for (int x = 0; x < NB; ++x)
@@ -327,7 +342,12 @@ __global__ void __launch_bounds__(F32<D>::kThreads, D == 64 ? 3 : 2) attn_prefil
             for (int e = 0; e < 2; ++e) {
                 float v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = (o[x][i][2 * r + e] * f0 + row[32 * x + 8 * t + 4 * e + i] * f1) * f;
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = o[x][i][2 * r + e] * f[0];
+#pragma unroll
+                    for (int k = 1; k < KG; ++k) v[i] += row[(k - 1) * T::kRows * JLD + 32 * x + 8 * t + 4 * e + i] * f[k];
+                    v[i] *= inv;
+                }
                 *reinterpret_cast<float4 *>(dst + 32 * x + 8 * t + 4 * e) = make_float4(v[0], v[1], v[2], v[3]);
             }
     }
@@ -340,14 +360,14 @@ int group_shift_of(const AttnArgs &a) {
     return gs;
 }
 
-template <int D>
-cudaError_t launch_f32(const AttnArgs &a, cudaStream_t stream) {
-    using T = F32<D>;
+template <int D, int KG>
+cudaError_t launch_f32_kg(const AttnArgs &a, cudaStream_t stream) {
+    using T = F32<D, KG>;
     static std::atomic<uint64_t> ready{0};
-    auto kern = attn_prefill_f32<D>;
+    auto kern = attn_prefill_f32<D, KG>;
     const cudaError_t e = allow_smem(kern, ready, T::kSmem);
     if (e != cudaSuccess) return e;
-    const int gs = group_shift_of(a);
+    const int gs = std::min(group_shift_of(a), KG == 2 ? 5 : 4);
     CUtensorMap km, vm;
     if (!page_map(&km, a.k_pages, D, a, false, 16) || !page_map(&vm, a.v_pages, D, a, false, 16)) return cudaErrorInvalidValue;
     const long long blocks = query_tiles(a, T::kRows >> gs) * (a.Hq >> gs);
@@ -355,6 +375,21 @@ cudaError_t launch_f32(const AttnArgs &a, cudaStream_t stream) {
     const unsigned grid = (unsigned)blocks;
     kern<<<grid, T::kThreads, T::kSmem, stream>>>(km, vm, a, gs);
     return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_f32(const AttnArgs &a, cudaStream_t stream) {
+    const int gs = group_shift_of(a);
+    int sms = 0;
+    const cudaError_t e = device_sms(&sms);
+    if (e != cudaSuccess) return e;
+    // Calls whose blocks of 32 rows are resident at once anyway take blocks
+    // of 16 rows and four groups of keys: half the time of the longest block
+    // (head size 128, 8 heads, 1024 new tokens: 98 -> 68 us; 475: 49 -> 35;
+    // 3 x 512 are past the bound, 66 against 70).  At head size 256 one such
+    // block fills an SM (512 tokens: 100 -> 68 us, 2 x 512: 124 against 135).
+    if (query_tiles(a, 32 >> gs) * (a.Hq >> gs) <= (D == 256 ? 1LL : 2LL) * sms) return launch_f32_kg<D, 4>(a, stream);
+    return launch_f32_kg<D, 2>(a, stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -385,6 +385,27 @@ def test_prefill(new, start, Hq, Hkv, D, page, window, softcap, io):
     no_device_errors()
 
 
+# The same operator where calls are split differently: many rows (blocks of 32
+# FP32 rows, several blocks to an SM), and few rows behind long contexts.
+@pytest.mark.parametrize("new,start,Hq,Hkv,D,page,window,softcap,io", [
+    ([700, 1, 500], [3, 200, 0], 24, 8, 128, 16, 0, 0.0, F32),
+    ([640, 200], [0, 77], 32, 4, 64, 32, 150, 0.0, F32),
+    ([300, 333], [40, 0], 16, 16, 256, 64, 0, 20.0, F32),
+    ([900, 64, 1200], [100, 0, 7], 32, 4, 64, 32, 0, 0.0, BF),
+    ([900, 64, 1200], [100, 0, 7], 16, 16, 64, 16, 333, 30.0, BF),
+    ([2], [20000], 8, 2, 128, 64, 0, 0.0, BF),
+    ([3, 1, 17], [5000, 9000, 250], 6, 2, 64, 16, 0, 0.0, BF),
+    ([16, 16], [7000, 0], 4, 1, 256, 32, 0, 20.0, BF),
+    ([5, 40], [9000, 600], 4, 4, 128, 16, 1000, 0.0, BF),
+    ([5, 40], [9000, 600], 4, 4, 128, 16, 0, 0.0, F32),
+    ([2], [20000], 8, 2, 64, 64, 0, 30.0, F32),
+    ([1, 20, 3], [6000, 0, 100], 3, 1, 256, 128, 3000, 0.0, F32),
+    ([4, 4, 4], [100, -1, 3000], 2, 2, 128, 16, 0, 0.0, F32),
+])
+def test_prefill_splits(new, start, Hq, Hkv, D, page, window, softcap, io):
+    test_prefill(new, start, Hq, Hkv, D, page, window, softcap, io)
+
+
 def test_prefill_reports_bad_places():
     g = gen(8)
     cfg = lq.AttnConfig(2, 1, 64)
