@@ -21,9 +21,101 @@ struct BlockPlace {
     long long tile;
     int head;  // first of the block's heads
 };
-__device__ __forceinline__ BlockPlace place_of(const AttnArgs &a, int group_shift) {
-    const unsigned groups = (unsigned)a.Hq >> group_shift, tiles = gridDim.x / groups, t = blockIdx.x / groups;
-    return BlockPlace{(long long)(tiles - 1 - t), (int)((blockIdx.x - t * groups) << group_shift)};
+__device__ __forceinline__ BlockPlace place_of(const AttnArgs &a, int group_shift, int split) {
+    const unsigned block = blockIdx.x / (unsigned)split, groups = (unsigned)a.Hq >> group_shift;
+    const unsigned tiles = gridDim.x / ((unsigned)split * groups), t = block / groups;
+    return BlockPlace{(long long)(tiles - 1 - t), (int)((block - t * groups) << group_shift)};
+}
+
+// Few rows behind long contexts: the key tiles of a query tile are dealt out
+// to the `split` blocks of a cluster.  Each leaves its rows' unnormalised
+// outputs, maximum (in units of log2) and sum in its shared memory, rows
+// D + 4 floats apart at `part`, and every block joins the rows whose number is
+// its rank modulo the split, in the order of the ranks.
+__device__ __forceinline__ void my_keys(int &k_first, int &n, int split, uint32_t rank) {
+    const int first = (int)((long long)n * rank / split);
+    n = (int)((long long)n * (rank + 1) / split) - first;
+    k_first += first;
+}
+
+constexpr int kMaxSplit = 8;
+
+template <int D, bool BF16>
+__device__ __forceinline__ void join_split(uint32_t part, int rows, int group_shift, int split, uint32_t rank,
+                                           const AttnArgs &a, const QueryTile &qt, int h0) {
+    cluster_sync();
+    constexpr int CH = D / 4;
+    for (int i = threadIdx.x; i < (rows + split - 1) / split * CH; i += blockDim.x) {
+        const int R = i / CH * split + (int)rank, ch = i % CH;
+        if (R >= rows) continue;
+        const uint32_t row = part + R * (D + 4) * 4;
+        float2 ml[kMaxSplit];
+        float4 o[kMaxSplit];
+#pragma unroll
+        for (int k = 0; k < kMaxSplit; ++k) {
+            if (k >= split) break;
+            const uint32_t at = peer_addr(row, k);
+            ml[k] = peer_load2(at + D * 4);
+            o[k] = peer_load4(at + ch * 16);
+        }
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kMaxSplit; ++k)
+            if (k < split) top = fmaxf(top, ml[k].x);
+        if (top == -INFINITY) top = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kMaxSplit; ++k) {
+            if (k >= split) break;
+            const float f = ex2(ml[k].x - top);
+            sum = fmaf(ml[k].y, f, sum);
+            v.x = fmaf(o[k].x, f, v.x), v.y = fmaf(o[k].y, f, v.y), v.z = fmaf(o[k].z, f, v.z), v.w = fmaf(o[k].w, f, v.w);
+        }
+        const float inv = 1.0f / sum;
+        const size_t dst = ((size_t)(qt.base + qt.first + (R >> group_shift)) * a.Hq + h0 + (R & ((1 << group_shift) - 1))) * D + 4 * ch;
+        if constexpr (BF16) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv), hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + dst) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+        } else {
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + dst) = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        }
+    }
+    cluster_sync();  // until then the peers read this block's shared memory
+}
+
+// Blocks of a cluster for a grid of `blocks` that leaves SMs idle (`slots`
+// blocks fit at once), with at least a tile of 128 keys each if the contexts
+// filled their block tables; tiles that turn out to have no more than
+// kSplitMin keys are left to one of the blocks.  Clusters of 8 do not reach
+// all SMs of a processing cluster, hence the eighth that is kept back.
+// 16 new tokens behind 2,000, 20,000 and 100,000, 32 query and 8 key-value
+// heads at head size 128, BF16: 33, 259 and 1261 us without, 13, 44 and 170
+// us with clusters.
+int split_of(const AttnArgs &a, long long blocks, int rows, long long slots) {
+    long long reach = (long long)a.max_pages << a.page_shift;
+    if (a.window > 0) reach = std::min(reach, (long long)a.window + rows);
+    slots -= slots / 8;
+    int split = 1;
+    while (split < kMaxSplit && 2 * split * blocks <= slots && 2 * split * 128 <= reach) split *= 2;
+    return split;
+}
+
+// Launch as clusters of `split` blocks.
+template <typename... P, typename... A>
+cudaError_t launch_split(void (*kern)(P...), long long blocks, int split, int threads, int smem, cudaStream_t stream, const A &...args) {
+    if (blocks * split > 0x7fffffffLL) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks * split));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)split, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = split > 1;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
 }
 
 // ---------------------------------------------------------------------------
@@ -42,6 +134,7 @@ struct F32 {
     static constexpr int kBufs = D < 256 && KG == 2 ? 2 : 1;         // tiles of K, and of V, that a key group holds
     static constexpr int kSmem = 1024 + 2 * KG * kBufs * kHalfBytes + kRows * kLd * 4;
     static constexpr int kBlocks = D == 64 ? 3 : D == 256 && KG == 4 ? 1 : 2;  // on an SM
+    static constexpr int kSplitMin = 128;
 };
 
 // One block: 16 or 32 rows, each a (token, head) pair of heads that share a
@@ -55,7 +148,7 @@ struct F32 {
 template <int D, int KG>
 __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
     attn_prefill_f32(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                     const AttnArgs a, const int group_shift) {
+                     const AttnArgs a, const int group_shift, const int cluster) {
     using T = F32<D, KG>;
     constexpr int RG = T::kRowGroups, KT = T::kKeys, NB = T::kBoxes, NT = KT / 8, LD = T::kLd, NBUF = T::kBufs;
     extern __shared__ unsigned char smem_raw[];
@@ -63,7 +156,7 @@ __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
     float *qs = reinterpret_cast<float *>(ring + 2 * KG * NBUF * T::kHalfBytes);
     __shared__ uint64_t full[KG][2][2], empty[KG][2][2];  // [key group][K (and V with two buffers), V][buffer]
     __shared__ int find[T::kThreads / 32 + 6];
-    const BlockPlace at = place_of(a, group_shift);
+    const BlockPlace at = place_of(a, group_shift, cluster);
     const QueryTile qt = find_query_tile<T::kThreads>(a, T::kRows >> group_shift, at.tile, find);
     if (qt.rows <= 0) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -71,8 +164,15 @@ __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
     const int heads = 1 << group_shift, h0 = at.head, kv = h0 / (a.Hq / a.Hkv);
     const int p0 = qt.start + qt.first, len = p0 + qt.rows;  // keys any row sees: lo .. len - 1
     const int lo = a.window > 0 && p0 + 1 > a.window ? p0 + 1 - a.window : 0;
-    const int k_first = lo / KT, n = (len - 1) / KT - k_first + 1;
-
+    int k_first = lo / KT, n = (len - 1) / KT - k_first + 1;
+    __shared__ int split_of_tile;  // (not a register of the loop below)
+    {
+        const int split = n * KT > T::kSplitMin ? cluster : 1;
+        const uint32_t rank = cluster > 1 ? cluster_rank() : 0;
+        if (rank >= (uint32_t)split) return;
+        if (split > 1) my_keys(k_first, n, split, rank);
+        if (tid == 0) split_of_tile = split;
+    }
     if (tid < 4 * KG) mbar_init(&full[0][0][0] + tid, 1), mbar_init(&empty[0][0][0] + tid, RG);
     __syncthreads();
     // One lane of a key group fills its buffers for the group's i-th tile: K
@@ -301,6 +401,7 @@ __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
     }
     // join the two halves of the keys: group 1 hands over through shared memory
     __syncthreads();
+    const int split = split_of_tile;
     constexpr int JLD = D + 2;
     float *jo = reinterpret_cast<float *>(ring) + rg * 16 * JLD;
     if (kg > 0) {
@@ -317,40 +418,48 @@ __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
         }
     }
     __syncthreads();
-    if (kg > 0 || !ok) return;
+    if (kg == 0) {
+        // (out of time: NaN, which reaches the output of a split call)
+        if (!ok) m[0] = m[1] = NAN;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int R = 16 * rg + g + 8 * r, tok = R >> group_shift;
-        if (tok >= qt.rows) continue;
-        const float *row = jo + (g + 8 * r) * JLD;
-        float top = m[r], f[KG];
+        for (int r = 0; r < 2; ++r) {
+            const int R = 16 * rg + g + 8 * r, tok = R >> group_shift;
+            if (tok >= qt.rows) continue;
+            const float *row = jo + (g + 8 * r) * JLD;
+            float top = m[r], f[KG];
 #pragma unroll
-        for (int k = 1; k < KG; ++k) top = fmaxf(top, row[(k - 1) * T::kRows * JLD + D]);
-        const float base = top == -INFINITY ? 0.0f : top;
-        f[0] = ex2(m[r] - base);
-        float sum = l[r] * f[0];
+            for (int k = 1; k < KG; ++k) top = fmaxf(top, row[(k - 1) * T::kRows * JLD + D]);
+            const float base = top == -INFINITY ? 0.0f : top;
+            f[0] = ex2(m[r] - base);
+            float sum = l[r] * f[0];
 #pragma unroll
-        for (int k = 1; k < KG; ++k) {
-            f[k] = ex2(row[(k - 1) * T::kRows * JLD + D] - base);
-            sum += row[(k - 1) * T::kRows * JLD + D + 1] * f[k];
-        }
-        const float inv = 1.0f / sum;
-        float *dst = static_cast<float *>(a.o) + ((size_t)(qt.base + qt.first + tok) * a.Hq + h0 + (R & (heads - 1))) * D;
-#pragma unroll
-        for (int x = 0; x < NB; ++x)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[i] = o[x][i][2 * r + e] * f[0];
-#pragma unroll
-                    for (int k = 1; k < KG; ++k) v[i] += row[(k - 1) * T::kRows * JLD + 32 * x + 8 * t + 4 * e + i] * f[k];
-                    v[i] *= inv;
-                }
-                *reinterpret_cast<float4 *>(dst + 32 * x + 8 * t + 4 * e) = make_float4(v[0], v[1], v[2], v[3]);
+            for (int k = 1; k < KG; ++k) {
+                f[k] = ex2(row[(k - 1) * T::kRows * JLD + D] - base);
+                sum += row[(k - 1) * T::kRows * JLD + D + 1] * f[k];
             }
+            // the row's output or, in a split call, its part
+            const float inv = split > 1 ? 1.0f : 1.0f / sum;
+            float *dst = split > 1 ? qs + R * LD
+                                   : static_cast<float *>(a.o) + ((size_t)(qt.base + qt.first + tok) * a.Hq + h0 + (R & (heads - 1))) * D;
+            if (split == 1 && !ok) continue;
+#pragma unroll
+            for (int x = 0; x < NB; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[i] = o[x][i][2 * r + e] * f[0];
+#pragma unroll
+                        for (int k = 1; k < KG; ++k) v[i] += row[(k - 1) * T::kRows * JLD + 32 * x + 8 * t + 4 * e + i] * f[k];
+                        v[i] *= inv;
+                    }
+                    *reinterpret_cast<float4 *>(dst + 32 * x + 8 * t + 4 * e) = make_float4(v[0], v[1], v[2], v[3]);
+                }
+            if (split > 1 && t == 0) dst[D] = ok ? top : NAN, dst[D + 1] = sum;
+        }
     }
+    if (split > 1) join_split<D, false>(smem_u32(qs), qt.rows << group_shift, group_shift, split, cluster_rank(), a, qt, h0);
 }
 
 // log2 of the heads that share a block's rows: the power of two in Hq / Hkv, at most 32.
@@ -361,7 +470,7 @@ int group_shift_of(const AttnArgs &a) {
 }
 
 template <int D, int KG>
-cudaError_t launch_f32_kg(const AttnArgs &a, cudaStream_t stream) {
+cudaError_t launch_f32_kg(const AttnArgs &a, int sms, cudaStream_t stream) {
     using T = F32<D, KG>;
     static std::atomic<uint64_t> ready{0};
     auto kern = attn_prefill_f32<D, KG>;
@@ -371,10 +480,8 @@ cudaError_t launch_f32_kg(const AttnArgs &a, cudaStream_t stream) {
     CUtensorMap km, vm;
     if (!page_map(&km, a.k_pages, D, a, false, 16) || !page_map(&vm, a.v_pages, D, a, false, 16)) return cudaErrorInvalidValue;
     const long long blocks = query_tiles(a, T::kRows >> gs) * (a.Hq >> gs);
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const unsigned grid = (unsigned)blocks;
-    kern<<<grid, T::kThreads, T::kSmem, stream>>>(km, vm, a, gs);
-    return cudaGetLastError();
+    const int split = KG == 4 ? split_of(a, blocks, T::kRows >> gs, (long long)T::kBlocks * sms) : 1;
+    return launch_split(kern, blocks, split, T::kThreads, T::kSmem, stream, km, vm, a, gs, split);
 }
 
 template <int D>
@@ -388,8 +495,8 @@ cudaError_t launch_f32(const AttnArgs &a, cudaStream_t stream) {
     // (head size 128, 8 heads, 1024 new tokens: 98 -> 68 us; 475: 49 -> 35;
     // 3 x 512 are past the bound, 66 against 70).  At head size 256 one such
     // block fills an SM (512 tokens: 100 -> 68 us, 2 x 512: 124 against 135).
-    if (query_tiles(a, 32 >> gs) * (a.Hq >> gs) <= (D == 256 ? 1LL : 2LL) * sms) return launch_f32_kg<D, 4>(a, stream);
-    return launch_f32_kg<D, 2>(a, stream);
+    if (query_tiles(a, 32 >> gs) * (a.Hq >> gs) <= (D == 256 ? 1LL : 2LL) * sms) return launch_f32_kg<D, 4>(a, sms, stream);
+    return launch_f32_kg<D, 2>(a, sms, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -487,9 +594,13 @@ __device__ __forceinline__ f32x2 capped(f32x2 x, const CapPoly &c) {
 // atoms of 1024 bytes (the stride byte offset).  MN-major, 128-byte swizzle:
 // blocks of 64 MN elements (128 bytes) by K rows, 8 K rows to an atom of 1024
 // bytes, `block` bytes from one block to the next (the leading byte offset).
+// Descriptors hold 18 bits of an address: above them the address of a block in
+// a cluster has its rank.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
-__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t block) { return (saddr >> 4) | (block >> 4) << 16; }
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4 | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t block) {
+    return (saddr & 0x3FFFFu) >> 4 | (block >> 4) << 16;
+}
 
 // D (TMEM) = A B (+ D when `add`), BF16, issued by one thread; A from shared
 // memory or, with its weights, from TMEM.
@@ -522,6 +633,7 @@ struct Tc {
     static constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
     static constexpr int kThreads = (kSoftWarps + 2) * 32;
     static constexpr int kSmem = 1024 + kStreams * kQBytes + kSlots * kSlotBytes;
+    static_assert(kStreams * 128 * (D + 4) * 4 <= kSmem - 1024, "the parts of a split call take the operands' place");
     // TMEM columns: the score tiles, whose first half the weights overwrite,
     // then the outputs
     static constexpr uint32_t kColS = 0, kColO = kStreams * kTiles * kKeys;
@@ -530,6 +642,7 @@ struct Tc {
     // on the SM keeps its softmax pipes busy (2 x 4096 tokens on a 4096-token
     // prefix, 32 heads: 752 -> 504 us; one block of four streams: 688).
     static constexpr int kBlocks = 512 / kCols;
+    static constexpr int kSplitMin = 256;
 };
 
 struct TcBars {
@@ -541,7 +654,8 @@ struct TcBars {
 template <int D, int NS, bool CAP>
 __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
     attn_prefill_tc(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                    const __grid_constant__ CUtensorMap vmap, const AttnArgs a, const int group_shift, const int box_shift) {
+                    const __grid_constant__ CUtensorMap vmap, const AttnArgs a, const int group_shift, const int box_shift,
+                    const int cluster) {
     using T = Tc<D, NS>;
     constexpr int KT = T::kKeys, NH = T::kHalves;
     extern __shared__ unsigned char smem_raw[];
@@ -554,7 +668,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
     const int tokens = 128 * NS >> group_shift;  // of a block
     if (warp == T::kMmaWarp) tmem_alloc(&tmem_slot, T::kCols);
     if (tid == 0) prefetch_map(&qmap), prefetch_map(&kmap), prefetch_map(&vmap);
-    const BlockPlace at = place_of(a, group_shift);
+    const BlockPlace at = place_of(a, group_shift, cluster);
     const QueryTile qt = find_query_tile<T::kThreads>(a, tokens, at.tile, find);
     if (qt.rows <= 0) {
         if (warp == T::kMmaWarp) tmem_dealloc(tmem_slot, T::kCols);
@@ -565,7 +679,14 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
     const int lo = a.window > 0 && p0 + 1 > a.window ? p0 + 1 - a.window : 0;
     // (streams without rows are left out)
     const int streams = (qt.rows * NS + tokens - 1) / tokens;
-    const int k_first = lo / KT, n = (len - 1) / KT - k_first + 1;
+    int k_first = lo / KT, n = (len - 1) / KT - k_first + 1;
+    const int split = n * KT > T::kSplitMin ? cluster : 1;
+    const uint32_t rank = cluster > 1 ? cluster_rank() : 0;
+    if (rank >= (uint32_t)split) {
+        if (warp == T::kMmaWarp) tmem_dealloc(tmem_slot, T::kCols);
+        return;
+    }
+    if (split > 1) my_keys(k_first, n, split, rank);
 
     if (tid < (int)(sizeof(TcBars) / sizeof(uint64_t))) {
         // a thread per barrier (each initialisation ends in a fence)
@@ -579,7 +700,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
 
     if (warp == T::kLoadWarp) {
         // ------------------------------------------------------------ TMA
-        if (lane == 0) {
+        if (lane == 0 && n > 0) {
             mbar_arrive_expect_tx(&bars.q_full, NS * T::kQBytes);
             const int t0 = (int)(qt.base + qt.first), per = 128 >> group_shift;
             for (int s = 0; s < NS; ++s)
@@ -637,7 +758,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
         };
         // in the order the MMA lane takes them
         int z = map_row(0, page_of(0)), page = page_of(1);
-        bool ok = load(&kmap, 0, z, false);
+        bool ok = n > 0 && load(&kmap, 0, z, false);
         for (int j = 0; ok && j < n; ++j) {
             const int zv = z;
             if (T::kTiles == 1) ok = load(&vmap, j, zv, true);
@@ -682,7 +803,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
         };
         auto wait = [&](uint64_t *bar, int parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity)) != 0; };
         int ks = 0, vs = 0;
-        bool ok = wait(&bars.q_full, 0) && take(ks);
+        bool ok = n > 0 && wait(&bars.q_full, 0) && take(ks);
         tc_fence_after_sync();
         if (ok && elect_one()) {
 #pragma unroll
@@ -865,8 +986,26 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
             apart(add2(sum0, sum1), sa0, sb0);
             l += sa0 + sb0;
         }
-        if (ok && bar_wait(&bars.o_done[s], T::kTiles == 2 ? (n - 1) & 1 : 0)) {
-            tc_fence_after_sync();
+        ok = ok && (n == 0 || bar_wait(&bars.o_done[s], T::kTiles == 2 ? (n - 1) & 1 : 0));
+        tc_fence_after_sync();
+        if (split > 1) {
+            // all products are done with the operands once every stream is
+            // here: the parts go in their place
+            asm volatile("bar.sync 1, %0;" ::"r"(128 * streams) : "memory");
+            float *row = reinterpret_cast<float *>(qs) + R * (D + 4);
+#pragma unroll 1
+            for (int k = 0; k < D; k += 16) {
+                float o[16];
+                if (n > 0) tmem_load_row(oa + k, o);
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<float4 *>(row + k + i) =
+                        n > 0 ? make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+            // (out of time: NaN)
+            row[D] = ok ? m * c : NAN;
+            row[D + 1] = l;
+        } else if (ok) {
             const float f = 1.0f / l;
             __nv_bfloat16 *op = static_cast<__nv_bfloat16 *>(a.o) + ((size_t)(qt.base + qt.first + tok) * a.Hq + head) * D;
 #pragma unroll 1
@@ -887,6 +1026,10 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
                 }
             }
         }
+    }
+    if (split > 1) {
+        __syncwarp();
+        join_split<D, true>(smem_u32(qs), qt.rows << group_shift, group_shift, split, rank, a, qt, h0);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -923,11 +1066,12 @@ cudaError_t launch_tc(const AttnArgs &a, cudaStream_t stream) {
     if (!query_map(&qm, a, D, 1 << gs) || !page_map(&km, a.k_pages, D, a, true, 1 << bs) ||
         !page_map(&vm, a.v_pages, D, a, true, 1 << bs))
         return cudaErrorInvalidValue;
+    int sms = 0;
+    const cudaError_t es = device_sms(&sms);
+    if (es != cudaSuccess) return es;
     const long long blocks = query_tiles(a, 128 * NS >> gs) * (a.Hq >> gs);
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const unsigned grid = (unsigned)blocks;
-    kern<<<grid, T::kThreads, T::kSmem, stream>>>(qm, km, vm, a, gs, bs);
-    return cudaGetLastError();
+    const int split = split_of(a, blocks, 128 * NS >> gs, (long long)T::kBlocks * sms);
+    return launch_split(kern, blocks, split, T::kThreads, T::kSmem, stream, qm, km, vm, a, gs, bs, split);
 }
 
 template <int D>
