@@ -23,12 +23,19 @@
 // softmax weights enter the product with V as two BF16 parts (p = hi + lo,
 // relative error 2^-17), so the output carries one rounding, its own.  With at
 // most 8 heads per key-value head the lower 8 rows hold hi, the upper 8 lo,
-// of one and the same MMA.  Warp MMAs and not tcgen05: a tile needs 2 MMAs
-// per token, a fifth of what the warp path can issue while DRAM delivers the
-// token, and accumulators in registers keep the warps independent.
+// of one and the same MMA.  Warp MMAs and not tcgen05: a token of a
+// key-value head needs D / 64 of them, a fifth of what the warp path can issue
+// while DRAM delivers the token, and accumulators in registers keep the warps
+// independent.
 //
-// FP32 (F32Core): the same with operands split into TF32 parts, 8 query heads
-// at a time.
+// FP32 (F32Core): the same with operands split into two TF32 parts, 8 query
+// heads at a time.
+//
+// Measured on B200 (6.55 TB/s copy): BF16, 256 sequences of 15 to 4,095
+// tokens, 32 query and 8 key-value heads, head size 128: 320 us, 6.1 TB/s;
+// three sequences of 90,000 to 131,071, 16 and 2 heads, head size 256: 114
+// us, 6.0 TB/s; one of 700 tokens: 9.3 us, the latency of the two launches.
+// The tensor pipe is busy 20 % of the time, 21 % of the issue slots are used.
 #include "lq_attn_common.cuh"
 
 namespace lq {
@@ -298,7 +305,7 @@ struct Bf16Core {
 };
 
 // The same over tiles of FP32 rows, 8 query rows.  Every FP32 operand enters
-// the TF32 MMAs as two parts, x = hi + lo with hi its upper 11 bits: the upper
+// the TF32 MMAs as two parts, x = hi + lo with hi rounded to 11 bits: the upper
 // 8 rows of the A operand hold the hi parts and the lower 8 the lo parts of
 // the 8 query rows (or of their weights), and B comes once as hi and once as
 // lo, so two MMAs give all four products.  A row of scratch (head size 256) is

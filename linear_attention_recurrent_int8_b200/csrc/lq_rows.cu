@@ -12,6 +12,15 @@
 // table row is loaded once per lane and used for all of the block's rows,
 // and the row loads (up to four per lane in flight) do not wait for the
 // chain cu_tokens -> pos -> block_table / table.
+//
+// Measured on B200 (6.55 TB/s copy): 16,384 tokens of 32 + 32 heads, head size
+// 128, BF16, L2 norm: 85.5 us, 6.2 TB/s of algorithmic traffic.  9,458 ragged
+// tokens of 16 + 2 + 2 heads at head size 256, RMS norm, rotation, appended:
+// 45 us, 4.3 TB/s; there instruction issue bounds it (65 % of the slots:
+// conversions, norm and rotation of 8 channels are about 40 instructions).
+// Two tokens: 2.1 us.  Lanes of 16 channels (52 us appended), several tokens
+// to a block (46 to 72) and a shared-memory ring filled by bulk copies (57)
+// were slower.
 #include "lq_attn.h"
 #include "lq_common.cuh"
 
