@@ -621,3 +621,163 @@ def test_long_append_reports_bad_places():
     gone[3 * n + 980:] = True
     assert (qo[gone.cuda()] == 3.0).all() and (qo[~gone.cuda()] != 3.0).any(-1).any(-1).all()
     assert int((~pg.v.isnan()).sum()) == int((~gone).sum()) * 8 * 128
+
+
+# ------------------------------------------------------------------ calls that share the GPU, far pages, odd scores
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_split_prefill_in_a_graph_and_on_another_stream(io):
+    """Few rows behind long contexts, captured once and replayed with other
+    positions (from a few keys to all), equal to the eager calls and right."""
+    g = gen(51)
+    cfg = lq.AttnConfig(8, 2, 128, io_dtype=io)
+    B, n, page, width = 2, 3, 32, 200
+    pg = Paged(g, cfg, B, page, width)
+    pg.fill(g, [width * page] * B)
+    q = randn(g, B * n, 8, 128, dtype=DT[io], scale=2.0)
+    o = torch.zeros_like(q)
+    pos = torch.tensor([0, 5000], dtype=torch.int32, device="cuda")
+    lq.lq_attn_prefill(cfg, pg.cache, pos, None, q, o)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lq.lq_attn_prefill(cfg, pg.cache, pos, None, q, o)
+    for places in ([0, 5000], [6397, 255], [130, -1], [2047, 400]):
+        pos.copy_(torch.tensor(places, dtype=torch.int32))
+        o.fill_(3.0)
+        graph.replay()
+        got = o.clone()
+        o.fill_(3.0)
+        other = torch.cuda.Stream()
+        other.wait_stream(torch.cuda.current_stream())
+        lq.lq_attn_prefill(cfg, pg.cache, pos, None, q, o, stream=other)
+        torch.cuda.current_stream().wait_stream(other)
+        assert torch.equal(got, o)
+        for b in range(B):
+            if places[b] < 0:
+                assert (o[b * n:(b + 1) * n] == 3.0).all()
+            else:
+                check_attention(cfg, pg, q[b * n:(b + 1) * n], o[b * n:(b + 1) * n], b, places[b],
+                                2.0 ** -8 if io == BF else 0.0, f"{places} sequence {b}")
+    no_device_errors()
+
+
+def test_calls_on_two_streams_at_once():
+    """Decode calls with workspaces of their own and split prefill calls, on two
+    streams at once, give what they give alone."""
+    g = gen(52)
+    jobs = []
+    for D, Hq, Hkv in ((128, 8, 2), (256, 4, 1)):
+        cfg = lq.AttnConfig(Hq, Hkv, D)
+        pg = Paged(g, cfg, 3, 64, 100)
+        pg.fill(g, [6400] * 3)
+        q = randn(g, 3, Hq, D, dtype=torch.bfloat16, scale=2.0)
+        pos = torch.tensor([6399, 17, 3000], dtype=torch.int32, device="cuda")
+        ws = torch.empty(lq.lq_attn_workspace_bytes(cfg, 3), dtype=torch.uint8, device="cuda")
+        jobs.append((cfg, pg, pos, q, torch.empty_like(q), torch.empty_like(q), ws, torch.cuda.Stream()))
+
+    def calls(job, stream):
+        cfg, pg, pos, q, od, op, ws, _ = job
+        lq.lq_attn_decode(cfg, pg.cache, pos, q, od, ws, stream=stream)
+        lq.lq_attn_prefill(cfg, pg.cache, pos, None, q, op, stream=stream)
+
+    alone = []
+    for job in jobs:
+        calls(job, None)
+        alone.append((job[4].clone(), job[5].clone()))
+        for b, p in enumerate((6399, 17, 3000)):
+            check_attention(job[0], job[1], job[3][b:b + 1], job[4][b:b + 1], b, p, 2.0 ** -17, "decode")
+            check_attention(job[0], job[1], job[3][b:b + 1], job[5][b:b + 1], b, p, 2.0 ** -8, "prefill")
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for job in jobs:
+            calls(job, job[7])
+    torch.cuda.synchronize()
+    for job, (od, op) in zip(jobs, alone):
+        assert torch.equal(job[4], od) and torch.equal(job[5], op)
+    no_device_errors()
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_the_largest_batch(io):
+    """4,096 sequences: decode, and prefill of one token each, idle slots among them."""
+    g = gen(53)
+    cfg = lq.AttnConfig(3, 1, 64, io_dtype=io, window=20)
+    B = 4096
+    pos = torch.randint(-1, 31, (B,), generator=g, device="cuda", dtype=torch.int32)
+    pg = Paged(g, cfg, B, 16, 2)
+    pl = pos.tolist()
+    pg.fill(g, [p + 1 for p in pl])
+    q = randn(g, B, 3, 64, dtype=DT[io], scale=2.0)
+    od, op = torch.full_like(q, 3.0), torch.full_like(q, 3.0)
+    lq.lq_attn_decode(cfg, pg.cache, pos, q, od)
+    lq.lq_attn_prefill(cfg, pg.cache, pos, None, q, op)
+    assert (od[pos < 0] == 3.0).all() and (op[pos < 0] == 3.0).all()
+    for b in list(range(0, B, 97)) + [B - 1]:
+        if pl[b] >= 0:
+            check_attention(cfg, pg, q[b:b + 1], od[b:b + 1], b, pl[b], 2.0 ** -17 if io == BF else 0.0, f"decode {b}")
+            check_attention(cfg, pg, q[b:b + 1], op[b:b + 1], b, pl[b], 2.0 ** -8 if io == BF else 0.0, f"prefill {b}")
+    no_device_errors()
+
+
+def test_pages_past_32_bits_of_elements():
+    """A cache of more than 2^32 elements: append, decode and prefill at both of its ends."""
+    g = gen(54)
+    Hq, Hkv, D, page = 8, 4, 256, 256
+    cfg = lq.AttnConfig(Hq, Hkv, D)
+    P = (1 << 32) // (Hkv * D * page) + 40
+    k = torch.empty(P, Hkv, page, D, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    table = torch.tensor([[P - 1, 0, P - 2], [1, P - 30, 2]], dtype=torch.int32, device="cuda")
+    cache = lq.KvCache(cfg, k, v, table)
+    n = 700
+    kk, vv = (randn(g, 2 * n, Hkv, D, dtype=torch.bfloat16) for _ in range(2))
+    q = randn(g, 2 * n, Hq, D, dtype=torch.bfloat16, scale=2.0)
+    qo, o = torch.empty_like(q), torch.empty_like(q)
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    lq.lq_kv_append(cfg, cache, zero, None, q, kk, vv, None, None, None, qo)
+    lq.lq_attn_prefill(cfg, cache, zero, None, qo, o)
+    od = torch.empty(2, Hq, D, dtype=torch.bfloat16, device="cuda")
+    lq.lq_attn_decode(cfg, cache, zero + n - 1, qo.view(2, n, Hq, D)[:, -1].contiguous(), od)
+    assert torch.equal(qo, q)
+    pos = torch.arange(n, device="cuda")[:, None]
+    mask = torch.arange(n, device="cuda")[None] <= pos
+    for b in range(2):
+        rows = slice(b * n, (b + 1) * n)
+        for x, y in ((k, kk), (v, vv)):
+            got = x[table[b].long()].transpose(1, 2).reshape(-1, Hkv, D)[:n]
+            assert torch.equal(got, y[rows])
+        for h in range(Hq):
+            K, V = (x[rows, h // 2].double() for x in (kk, vv))
+            want, av, mag = ref.attend(q[rows, h].double(), K, V, mask, cfg.c().scale, 0.0)
+            within(o[rows, h], want, ref.attend_bound(want, av, mag, D, n, o.dtype, 0.0, 2.0 ** -8), f"prefill {b} {h}")
+            within(od[b, h], want[-1], ref.attend_bound(want[-1:], av[-1:], mag[-1:], D, n, o.dtype, 0.0, 2.0 ** -17)[0],
+                   f"decode {b} {h}")
+    no_device_errors()
+
+
+@pytest.mark.parametrize("io,D", [(BF, 64), (BF, 128), (BF, 256), (F32, 64), (F32, 256)])
+def test_prefill_infinite_scores(io, D):
+    """-inf scores weigh nothing, also where they fill the keys of whole blocks
+    of a split call; rows of nothing else are NaN, as their formula."""
+    g = gen(55)
+    cfg = lq.AttnConfig(2, 1, D, io_dtype=io)
+    n, new = 4000, 2
+    pg = Paged(g, cfg, 3, 16, -(-n // 16))
+    pg.fill(g, [n] * 3)
+    q = torch.zeros(3 * new, 2, D, dtype=DT[io], device="cuda")
+    q[..., 0] = 1.0
+    hit = torch.arange(n, device="cuda")
+    gone = (hit < 2500) | (hit % 3 == 0)
+    for b, t in ((0, hit[gone]), (1, hit)):
+        pg.k[pg.table[b].long()[t // 16], 0, t % 16, 0] = -math.inf
+    o = torch.empty_like(q)
+    lq.lq_attn_prefill(cfg, pg.cache, torch.full((3,), n - new, dtype=torch.int32, device="cuda"), None, q, o)
+    K, V = pg.dense(0, n)
+    mask = (~gone)[None] & (hit[None] <= n - new + torch.arange(new, device="cuda")[:, None])
+    for h in range(2):
+        want, av, mag = ref.attend(q[:new, h].double(), K[0].nan_to_num(neginf=-1e30), V[0], mask, cfg.c().scale, 0.0)
+        within(o[:new, h], want, ref.attend_bound(want, av, mag, D, n, o.dtype, 0.0, 2.0 ** -8 if io == BF else 0.0), "some -inf")
+    assert o[new:2 * new].isnan().all()
+    check_attention(cfg, pg, q[2 * new:], o[2 * new:], 2, n - new, 2.0 ** -8 if io == BF else 0.0, "clean")
+    no_device_errors()
