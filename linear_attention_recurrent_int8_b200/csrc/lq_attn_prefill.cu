@@ -28,17 +28,15 @@
 namespace lq {
 namespace {
 
-// What a block works on.  Tiles with the most keys before them (the last of a
-// sequence) go first, those of all heads together, so that the last blocks to
-// start are short ones.
+// What a block works on: the heads of a tile one after the other.
 struct BlockPlace {
-    long long tile;
+    long long turn, tiles;
     int head;  // first of the block's heads
 };
 __device__ __forceinline__ BlockPlace place_of(const AttnArgs &a, int group_shift, int split) {
     const unsigned block = blockIdx.x / (unsigned)split, groups = (unsigned)a.Hq >> group_shift;
     const unsigned tiles = gridDim.x / ((unsigned)split * groups), t = block / groups;
-    return BlockPlace{(long long)(tiles - 1 - t), (int)((block - t * groups) << group_shift)};
+    return BlockPlace{t, tiles, (int)((block - t * groups) << group_shift)};
 }
 
 // Few rows behind long contexts: the key tiles of a query tile are dealt out
@@ -171,7 +169,7 @@ __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
     __shared__ uint64_t full[KG][2][2], empty[KG][2][2];  // [key group][K (and V with two buffers), V][buffer]
     __shared__ int find[T::kThreads / 32 + 6];
     const BlockPlace at = place_of(a, group_shift, cluster);
-    const QueryTile qt = find_query_tile<T::kThreads>(a, T::kRows >> group_shift, at.tile, find);
+    const QueryTile qt = find_query_tile<T::kThreads, (T::kBlocks > 1)>(a, T::kRows >> group_shift, at.turn, at.tiles, find);
     if (qt.rows <= 0) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rg = warp % RG, kg = warp / RG;
@@ -683,8 +681,9 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
     if (warp == T::kMmaWarp) tmem_alloc(&tmem_slot, T::kCols);
     if (tid == 0) prefetch_map(&qmap), prefetch_map(&kmap), prefetch_map(&vmap);
     const BlockPlace at = place_of(a, group_shift, cluster);
-    const QueryTile qt = find_query_tile<T::kThreads>(a, tokens, at.tile, find);
+    const QueryTile qt = find_query_tile<T::kThreads, (T::kBlocks > 1)>(a, tokens, at.turn, at.tiles, find);
     if (qt.rows <= 0) {
+        __syncthreads();
         if (warp == T::kMmaWarp) tmem_dealloc(tmem_slot, T::kCols);
         return;
     }
@@ -697,6 +696,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
     const int split = n * KT > T::kSplitMin ? cluster : 1;
     const uint32_t rank = cluster > 1 ? cluster_rank() : 0;
     if (rank >= (uint32_t)split) {
+        __syncthreads();
         if (warp == T::kMmaWarp) tmem_dealloc(tmem_slot, T::kCols);
         return;
     }
