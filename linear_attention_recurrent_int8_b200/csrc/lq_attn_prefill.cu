@@ -504,10 +504,13 @@ cudaError_t launch_f32(const AttnArgs &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     // Calls whose blocks of 32 rows are resident at once anyway take blocks
     // of 16 rows and four groups of keys: half the time of the longest block
-    // (head size 128, 8 heads, 1024 new tokens: 98 -> 68 us; 475: 49 -> 35;
-    // 3 x 512 are past the bound, 66 against 70).  At head size 256 one such
-    // block fills an SM (512 tokens: 100 -> 68 us, 2 x 512: 124 against 135).
-    if (query_tiles(a, 32 >> gs) * (a.Hq >> gs) <= (D == 256 ? 1LL : 2LL) * sms) return launch_f32_kg<D, 4>(a, sms, stream);
+    // (8 heads, 475 new tokens: 49 -> 35 us at head size 128; 1400 at 64: 86
+    // -> 66; past the bound 4 x 512 at 64 take 44 against 53, 3 x 512 at 128
+    // 62 against 70).  At head size 256 one such block fills an SM (512
+    // tokens: 100 -> 68 us, 2 x 512: 124 against 135).  Short windows leave
+    // little to divide (2 x 600 tokens, window 200: 36 against 42 us).
+    const long long limit = a.window > 0 && a.window <= 512 ? 1 : F32<D, 4>::kBlocks;
+    if (query_tiles(a, 32 >> gs) * (a.Hq >> gs) <= limit * sms) return launch_f32_kg<D, 4>(a, sms, stream);
     return launch_f32_kg<D, 2>(a, sms, stream);
 }
 
