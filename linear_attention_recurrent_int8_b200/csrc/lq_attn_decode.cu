@@ -19,6 +19,12 @@
 // parts (o, m, sum) in the workspace that a second launch joins in the order
 // of the line, so results do not depend on scheduling.
 //
+// Where a key-value head has more query heads than the rows of a warp (16 or
+// 8), a run goes to as many warps of neighbouring SMs, which walk it side by
+// side, so that the second reads find part of it in the L2 cache (24 heads,
+// BF16, 800 MB: 256 -> 203 us at head size 128 against a line with a run for
+// each row group).
+//
 // BF16 (Bf16Core): query heads are the rows of a 16-row warp MMA.  The
 // softmax weights enter the product with V as two BF16 parts (p = hi + lo,
 // relative error 2^-17), so the output carries one rounding, its own.  With at
@@ -73,10 +79,10 @@ template <int D, int RU>
 __host__ __device__ constexpr size_t part_floats() { return (size_t)RU * (D + 2); }
 
 struct DecodePlan {
-    int units;       // row groups of all key-value heads of a sequence
-    int per_kv;      // row groups of a key-value head
+    int units;       // key-value heads of a sequence
+    int per_kv;      // row groups of a key-value head, a warp of the team each
     int stages;
-    int workers;
+    int teams;       // of per_kv warps; a run of the line each
     int min_tiles;   // tiles of the shortest run
 };
 
@@ -97,7 +103,7 @@ __device__ __forceinline__ long long divide(long long x, int y) {
 
 // A place on the line of tiles.
 struct Cursor {
-    int b, u, t, n, len, lo, t0;  // sequence, row group, tile, tiles of the pair, visible range, first tile
+    int b, u, t, n, len, lo, t0;  // sequence, key-value head, tile, tiles of the pair, visible range, first tile
 };
 
 template <int TOK>
@@ -567,7 +573,7 @@ __global__ void __launch_bounds__(Tile<D, BF16>::kWarps * 32, 1)
     }
     __syncthreads();
     const long long total = (long long)prefix[a.B] * pl.units;
-    long long per = divide(total + pl.workers - 1, pl.workers);
+    long long per = divide(total + pl.teams - 1, pl.teams);
     if (per < pl.min_tiles) per = pl.min_tiles;
     if (blockIdx.x == 0) {
         int *h = reinterpret_cast<int *>(a.ws);
@@ -575,9 +581,10 @@ __global__ void __launch_bounds__(Tile<D, BF16>::kWarps * 32, 1)
         if (tid == 0) h[a.B + 1] = (int)per;
     }
     // runs go to the SMs in turn, so that a short line spreads over all of them
-    const int worker = warp * gridDim.x + blockIdx.x;
-    const long long x0 = (long long)worker * per;
-    if (x0 >= total) return;
+    const int worker = warp * gridDim.x + blockIdx.x, team = pl.per_kv == 1 ? worker : worker / pl.per_kv;
+    const int group = worker - team * pl.per_kv;
+    const long long x0 = (long long)team * per;
+    if (x0 >= total || team >= pl.teams) return;
     const int run = (int)(total - x0 < per ? total - x0 : per);
 
     unsigned char *my_ring = ring + warp * pl.stages * T::kStageBytes;
@@ -601,9 +608,8 @@ __global__ void __launch_bounds__(Tile<D, BF16>::kWarps * 32, 1)
     // prepared inside that lane's branch they took about 900 cycles a tile.
     const uint32_t ring_addr = __shfl_sync(0xffffffffu, smem_u32(my_ring), 0), full_addr = __shfl_sync(0xffffffffu, smem_u32(full), 0);
     auto issue = [&]() {
-        const int kv = pl.per_kv == 1 ? pc.u : pc.u / pl.per_kv;
         const bool bad = page < 0 || page >= a.num_pages;
-        const int z = __shfl_sync(0xffffffffu, bad ? -1 : page * a.Hkv + kv, 0);
+        const int z = __shfl_sync(0xffffffffu, bad ? -1 : page * a.Hkv + pc.u, 0);
         const int row = __shfl_sync(0xffffffffu, ((pc.t0 + pc.t) * TOK) & (a.page_size - 1), 0);
         const uint32_t dst = ring_addr + fill * T::kStageBytes, bar = full_addr + fill * 8;
         if (elect_one()) {
@@ -625,9 +631,8 @@ __global__ void __launch_bounds__(Tile<D, BF16>::kWarps * 32, 1)
     bool fresh = false, whole = false;  // whole: the run holds the pair's first tile
     int head0 = 0, rows = 0;
     auto begin = [&]() {
-        const int kv = c.u / pl.per_kv, first = (c.u - kv * pl.per_kv) * RU;
-        head0 = kv * G + first;
-        rows = min(RU, G - first);
+        head0 = c.u * G + group * RU;
+        rows = min(RU, G - group * RU);
         core.begin(a, c.b, head0, rows, lane, sc);
         whole = c.t == 0;
         fresh = false;
@@ -669,7 +674,7 @@ __global__ void __launch_bounds__(Tile<D, BF16>::kWarps * 32, 1)
 
 // The parts of one query head's output.
 struct JoinJob {
-    int b, head, row, first, parts;  // sequence, head, its row of the group, first worker, number of parts
+    int b, head, group, row, first, parts;  // sequence, head, its row group and row in it, first team, number of parts
 };
 
 template <int RU>
@@ -682,16 +687,17 @@ __device__ __forceinline__ JoinJob join_job(const AttnArgs &a, const DecodePlan 
     if (n == 0) return j;
     const int G = a.Hq / a.Hkv, kv = j.head / G, in = j.head - kv * G;
     j.row = in % RU;
-    const long long s0 = (long long)p0 * pl.units + (long long)(kv * pl.per_kv + in / RU) * n;
+    j.group = in / RU;
+    const long long s0 = (long long)p0 * pl.units + (long long)kv * n;
     j.first = (int)(s0 / per);
     j.parts = (int)((s0 + n - 1) / per) - j.first + 1;
     return j;
 }
 
 template <int D, int RU>
-__device__ __forceinline__ const float *join_part(const AttnArgs &a, const JoinJob &j, int i) {
+__device__ __forceinline__ const float *join_part(const AttnArgs &a, const DecodePlan &pl, const JoinJob &j, int i) {
     // the first part is in its worker's second slot, the others in their worker's first
-    return reinterpret_cast<const float *>(a.ws + ws_header(a.B)) + ((size_t)(j.first + i) * 2 + (i == 0)) * part_floats<D, RU>();
+    return reinterpret_cast<const float *>(a.ws + ws_header(a.B)) + (((size_t)(j.first + i) * pl.per_kv + j.group) * 2 + (i == 0)) * part_floats<D, RU>();
 }
 
 // Joins the parts of the query heads, each sum in a fixed order.  A block takes
@@ -713,7 +719,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, const 
     const int c0 = JB == 1 ? blockIdx.x % (D / NC) * NC : 0;
     if (JB > 1 && mine.parts > 1 && mine.parts <= kFew) {
         const int x = lane < mine.parts ? lane : 0;
-        const float2 ml = *reinterpret_cast<const float2 *>(join_part<D, RU>(a, mine, x) + RU * D + 2 * mine.row);
+        const float2 ml = *reinterpret_cast<const float2 *>(join_part<D, RU>(a, pl, mine, x) + RU * D + 2 * mine.row);
         float m = group_max<32>(ml.x);
         if (m == -INFINITY) m = 0.0f;
         const float f = lane < mine.parts ? ex2(ml.x - m) : 0.0f;
@@ -723,7 +729,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, const 
 #pragma unroll 4
         for (int i = 0; i < mine.parts; ++i) {
             const float w = __shfl_sync(0xffffffffu, f, i), l = __shfl_sync(0xffffffffu, ml.y, i);
-            const float *p = join_part<D, RU>(a, mine, i) + mine.row * D + NV * lane;
+            const float *p = join_part<D, RU>(a, pl, mine, i) + mine.row * D + NV * lane;
             sum = fmaf(l, w, sum);
 #pragma unroll
             for (int e = 0; e < NV; e += 2) {
@@ -749,7 +755,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, const 
     for (; many; many &= many - 1) {
         const JoinJob j = JB == 1 ? mine : join_job<RU>(a, pl, (long long)blockIdx.x * JB + __ffs(many) - 1);
         float m = -INFINITY;
-        for (int i = tid; i < j.parts; i += 256) m = fmaxf(m, join_part<D, RU>(a, j, i)[RU * D + 2 * j.row]);
+        for (int i = tid; i < j.parts; i += 256) m = fmaxf(m, join_part<D, RU>(a, pl, j, i)[RU * D + 2 * j.row]);
         m = group_max<32>(m);
         if (lane == 0) red[warp] = m;
         __syncthreads();
@@ -761,7 +767,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, const 
         float sum = 0.0f;
 #pragma unroll 4
         for (int i = g; i < j.parts; i += NG) {
-            const float *p = join_part<D, RU>(a, j, i);
+            const float *p = join_part<D, RU>(a, pl, j, i);
             const float2 ml = *reinterpret_cast<const float2 *>(p + RU * D + 2 * j.row);
             const float4 v = *reinterpret_cast<const float4 *>(p + j.row * D + c0 + c);
             const float f = ex2(ml.x - m);
@@ -793,11 +799,12 @@ cudaError_t launch_decode_ru(const AttnArgs &a, cudaStream_t stream) {
     DecodePlan pl;
     const int G = a.Hq / a.Hkv;
     pl.per_kv = (G + RU - 1) / RU;
-    pl.units = a.Hkv * pl.per_kv;
+    pl.units = a.Hkv;
     pl.stages = (kSmemLimit - fixed_smem<D, BF16>(a.B)) / (T::kWarps * T::kStageBytes);
     if (pl.stages > kMaxStages) pl.stages = kMaxStages;
     if (pl.stages < 1) return cudaErrorInvalidConfiguration;
-    pl.workers = sms * T::kWarps;
+    pl.teams = sms * T::kWarps / pl.per_kv;
+    if (pl.teams < 1) return cudaErrorInvalidConfiguration;
     pl.min_tiles = 2;
     CUtensorMap km, vm;
     if (!page_map(&km, a.k_pages, D, a, BF16, T::kTok) || !page_map(&vm, a.v_pages, D, a, BF16, T::kTok))
@@ -809,7 +816,7 @@ cudaError_t launch_decode_ru(const AttnArgs &a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     // a block per head while they fill the GPU about once, else one for 8
     const int jobs = a.B * a.Hq;
-    const bool few = jobs <= pl.workers;
+    const bool few = jobs <= sms * T::kWarps;
     cfg.gridDim = dim3((unsigned)(few ? jobs * (D / 64) : (jobs + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
