@@ -14,7 +14,7 @@
 // chain cu_tokens -> pos -> block_table / table.
 //
 // Measured on B200 (6.55 TB/s copy): 16,384 tokens of 32 + 32 heads, head size
-// 128, BF16, L2 norm: 85.5 us, 6.2 TB/s of algorithmic traffic.  9,458 ragged
+// 128, BF16, L2 norm: 80 us, 6.6 TB/s of algorithmic traffic.  9,458 ragged
 // tokens of 16 + 2 + 2 heads at head size 256, RMS norm, rotation, appended:
 // 45 us, 4.3 TB/s; there instruction issue bounds it (65 % of the slots:
 // conversions, norm and rotation of 8 channels are about 40 instructions).
@@ -113,8 +113,11 @@ __device__ __forceinline__ float rsqrt_normal(float x) {
 // heads (copied).  SPLIT (rotation by halves): the lanes of the rotated
 // channels hold 4 of the first half and their 4 partners of the second, so
 // that a pair needs no exchange and its cosine and sine are loaded once.
+// (Five blocks of 256 threads on an SM instead of four are worth up to 9 % to
+// BF16 rows with a rotation, 114 -> 104 us for 9,458 tokens of 32 + 8 heads at
+// head size 256; FP32 and appended rows would spill, 157 against 185 us.)
 template <int D, bool BF16, bool SPLIT, bool APPEND, int NR>
-__global__ void __launch_bounds__(256, NR == 4 ? 4 : 6) rows_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(256, NR == 4 ? (BF16 && !APPEND ? 5 : 4) : 6) rows_kernel(const RowsArgs a) {
     constexpr int L = D / 8;
     const int tid = threadIdx.x, l = tid & (L - 1);
     const int half = a.rot / 2;
@@ -195,6 +198,13 @@ __global__ void __launch_bounds__(256, NR == 4 ? 4 : 6) rows_kernel(const RowsAr
         load4(sn, row + half);
     }
 
+    // where the heads of the token go
+    char *const qdst = static_cast<char *>(a.q_out) + (size_t)t * a.Hq * (D * es);
+    char *const kdst = APPEND ? static_cast<char *>(a.k_pages) + page_row * (D * es)
+                              : static_cast<char *>(a.k_out) + (size_t)t * a.Hkv * (D * es);
+    char *const vdst = APPEND ? static_cast<char *>(a.v_pages) + page_row * (D * es) : nullptr;
+    const unsigned next = (APPEND ? a.page_size : 1) * (D * es);  // from a head to the next
+
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const int r = r0 + i * groups;
@@ -230,12 +240,8 @@ __global__ void __launch_bounds__(256, NR == 4 ? 4 : 6) rows_kernel(const RowsAr
         }
         if (r >= R) continue;
         const Raw<BF16> out = is_v ? raw[i] : pack<BF16>(x);
-        char *dst;
-        if (r < a.Hq) dst = static_cast<char *>(a.q_out) + ((size_t)t * a.Hq + r) * (D * es);
-        else if constexpr (APPEND) {
-            const int h = is_v ? r - a.Hq - a.Hkv : r - a.Hq;
-            dst = static_cast<char *>(is_v ? a.v_pages : a.k_pages) + (page_row + (size_t)h * a.page_size) * (D * es);
-        } else dst = static_cast<char *>(a.k_out) + ((size_t)t * a.Hkv + (r - a.Hq)) * (D * es);
+        char *dst = r < a.Hq ? qdst + r * (D * es) : kdst + (unsigned)(r - a.Hq) * next;
+        if (APPEND && is_v) dst = vdst + (unsigned)(r - a.Hq - a.Hkv) * next;
         store_raw<BF16, SPLIT>(dst, off0, off1, out);
     }
 }
@@ -247,8 +253,9 @@ cudaError_t launch_rows_d(const RowsArgs &a, cudaStream_t stream) {
     // one row per group while all of them fit on the GPU at once, else four
     const bool wide = (long long)a.tokens * R * L > 148LL * 2048;
     const int nr = wide ? 4 : 1;
-    int threads = (R + nr - 1) / nr * L;
-    threads = threads >= 256 ? 256 : (threads + 31) / 32 * 32;
+    // as few blocks of up to 256 threads as hold the token's rows, in equal shares
+    const int most = 256 / L * nr, blocks = (R + most - 1) / most;
+    const int threads = (((R + blocks - 1) / blocks + nr - 1) / nr * L + 31) / 32 * 32;
     const int rows = threads / L * nr;
     const dim3 grid((unsigned)a.tokens, (unsigned)((R + rows - 1) / rows));
     if (wide) rows_kernel<D, BF16, SPLIT, APPEND, 4><<<grid, threads, 0, stream>>>(a);

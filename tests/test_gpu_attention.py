@@ -781,3 +781,16 @@ def test_prefill_infinite_scores(io, D):
     assert o[new:2 * new].isnan().all()
     check_attention(cfg, pg, q[2 * new:], o[2 * new:], 2, n - new, 2.0 ** -8 if io == BF else 0.0, "clean")
     no_device_errors()
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,io", [(2000, 32, 8, BF), (900, 33, 11, F32), (3, 33, 11, BF), (1500, 40, 1, BF)])
+def test_norm_rows_in_shares(T, Hq, Hkv, io):
+    """Tokens whose heads take several blocks, in shares that do not divide them."""
+    test_norm_rotate(T, Hq, Hkv, 256, lq.LQ_NORM_RMS, True, 64, lq.LQ_ROT_HALVES, io)
+    test_norm_rotate(T, Hq, Hkv, 256, lq.LQ_NORM_L2, False, 256, lq.LQ_ROT_ADJACENT, io)
+
+
+@pytest.mark.parametrize("new,start,Hq,Hkv,io", [([700, 1, 500], [3, 60, 0], 32, 8, BF), ([1, 2, 1], [0, 15, -1], 33, 11, F32)])
+def test_append_rows_in_shares(new, start, Hq, Hkv, io):
+    for with_q in (True, False):
+        test_append(new, start, Hq, Hkv, 256, 32, lq.LQ_NORM_RMS, 64, lq.LQ_ROT_HALVES, io, with_q)
