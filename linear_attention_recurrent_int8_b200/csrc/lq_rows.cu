@@ -113,9 +113,9 @@ __device__ __forceinline__ float rsqrt_normal(float x) {
 // heads (copied).  SPLIT (rotation by halves): the lanes of the rotated
 // channels hold 4 of the first half and their 4 partners of the second, so
 // that a pair needs no exchange and its cosine and sine are loaded once.
-// (Five blocks of 256 threads on an SM instead of four are worth up to 9 % to
-// BF16 rows with a rotation, 114 -> 104 us for 9,458 tokens of 32 + 8 heads at
-// head size 256; FP32 and appended rows would spill, 157 against 185 us.)
+// (Five blocks of 256 threads on an SM instead of four are worth 4 % to BF16
+// rows with a rotation, 42 -> 40 us for 9,458 tokens of 32 + 8 heads at head
+// size 128; FP32 and appended rows would spill, 76 against 86 us.)
 template <int D, bool BF16, bool SPLIT, bool APPEND, int NR>
 __global__ void __launch_bounds__(256, NR == 4 ? (BF16 && !APPEND ? 5 : 4) : 6) rows_kernel(const RowsArgs a) {
     constexpr int L = D / 8;
@@ -253,7 +253,8 @@ cudaError_t launch_rows_d(const RowsArgs &a, cudaStream_t stream) {
     // one row per group while all of them fit on the GPU at once, else four
     const bool wide = (long long)a.tokens * R * L > 148LL * 2048;
     const int nr = wide ? 4 : 1;
-    // as few blocks of up to 256 threads as hold the token's rows, in equal shares
+    // as few blocks of up to 256 threads as hold the token's rows, in equal
+    // shares (48 rows of head size 256 as 24 + 24 and not 32 + 16: 120 -> 99 us)
     const int most = 256 / L * nr, blocks = (R + most - 1) / most;
     const int threads = (((R + blocks - 1) / blocks + nr - 1) / nr * L + 31) / 32 * 32;
     const int rows = threads / L * nr;
