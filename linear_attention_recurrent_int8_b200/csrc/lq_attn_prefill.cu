@@ -587,11 +587,18 @@ __device__ __forceinline__ void ex2_fma(f32x2 v, float &a, float &b) {
 
 // cap tanh(z x) in units of log2 for |z x| <= 3/4, as x times a polynomial in
 // x^2 whose coefficients hold z and the cap: tanh y = y + y^3 (c0 + c1 y^2 +
-// c2 y^4), least maximum error 5.6e-6.
+// c2 y^4), least maximum error 5.6e-6.  The coefficients hold powers of z up to
+// the 7th and the cap (1e-3 to 1e6): with z between 2^-14 and 2^14 all of them
+// are normal numbers; other z take capped_log2.
 constexpr float kTanhReach = 0.75f;
 struct CapPoly {
     float k[4];
 };
+// |x| up to which the polynomial serves (-1: not at all).
+__device__ __forceinline__ float cap_reach(float z) {
+    z = fabsf(z);
+    return z >= 1.0f / 16384.0f && z <= 16384.0f ? kTanhReach / z : -1.0f;
+}
 __device__ __forceinline__ CapPoly cap_poly(float z, float out) {
     const float z3 = z * z * z, z5 = z3 * z * z, z7 = z5 * z * z;
     return CapPoly{{out * z, out * z3 * -0.3327198326587677f, out * z5 * 0.1272989809513092f, out * z7 * -0.03519973158836365f}};
@@ -895,8 +902,8 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
         // masked score stays -inf), or 1 for capped scores
         const float c = CAP ? 1.0f : fmaxf(fabsf(a.scale * kLog2e), 1e-30f);
         const SoftCap cap = soft_cap(a.scale, a.softcap);
-        const CapPoly poly = cap_poly(a.scale / a.softcap, cap.out);
-        const float in_reach = kTanhReach * a.softcap / fabsf(a.scale);
+        const CapPoly poly = cap_poly(cap.in, cap.out);
+        const float in_reach = cap_reach(cap.in);
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int j = 0; j < n; ++j) {

@@ -1,0 +1,115 @@
+"""The softmax-attention operators at the ends of their ranges, and what their
+outputs must not depend on."""
+import math
+
+import pytest
+import torch
+
+import attnref as ref
+import linear_attention_recurrent_int8_b200 as lq
+import test_gpu_attention as base
+from test_gpu_attention import BF, DT, F32, Paged, check_attention, gen, no_device_errors, randn
+
+pytestmark = pytest.mark.gpu
+
+
+def split_of(io):
+    """Relative rounding of the prefill's softmax weights."""
+    return 2.0 ** -8 if io == BF else 0.0
+
+
+# ------------------------------------------------------------------ score caps
+
+# A cap as small as the header allows under a large scale: scale / cap to the
+# 7th power is past FP32, scale / cap itself is not.
+@pytest.mark.parametrize("io,D", [(BF, 64), (BF, 128), (BF, 256), (F32, 64)])
+@pytest.mark.parametrize("scale,softcap", [(1e3, 1e-3), (-1e6, 1e-3), (1e6, 1.0)])
+@pytest.mark.parametrize("size", [0.0, 1e-5, 1.0])
+def test_small_caps_under_large_scales(io, D, scale, softcap, size):
+    """Queries of zeros give the mean of the values, tiny and ordinary ones
+    the capped softmax."""
+    g = gen(61 + D)
+    cfg = lq.AttnConfig(4, 2, D, io_dtype=io, scale=scale, softcap=softcap)
+    n = 150
+    pg = Paged(g, cfg, 2, 16, 10)
+    # (powers of two in one channel: the scores' own rounding, which such a
+    # scale brings up to the size of the cap, is none)
+    pg.fill(g, [n, n])
+    p = torch.arange(n, device="cuda")
+    for b in range(2):
+        at = (pg.table[b].long()[p // 16], slice(None), p % 16)
+        k = torch.zeros(n, 2, D, dtype=DT[io], device="cuda")
+        k[..., 0] = torch.exp2(torch.randint(-3, 4, (n, 2), generator=g, device="cuda").float()).to(DT[io])
+        pg.k[at] = k
+    q = torch.zeros(40, 4, D, dtype=DT[io], device="cuda")
+    q[..., 0] = size * randn(g, 40, 4, dtype=DT[io])
+    o = torch.empty_like(q)
+    lq.lq_attn_prefill(cfg, pg.cache, torch.full((2,), n - 20, dtype=torch.int32, device="cuda"), None, q, o)
+    od = torch.empty(2, 4, D, dtype=DT[io], device="cuda")
+    lq.lq_attn_decode(cfg, pg.cache, torch.full((2,), n - 1, dtype=torch.int32, device="cuda"), q[:2].contiguous(), od)
+    for b in range(2):
+        rows = slice(20 * b, 20 * b + 20)
+        # one product a score: its rounding, that of scale / cap and of their
+        # product move y = s / cap by 3 half steps, so a score by at most
+        # cap |y| (1 - tanh^2 y) 3 2^-24 < 2 cap 2^-24, inside the bound's 8
+        check_exact_scores(cfg, pg, q[rows], o[rows], b, n - 20, split_of(io))
+        check_exact_scores(cfg, pg, q[b:b + 1], od[b:b + 1], b, n - 1, 2.0 ** -17 if io == BF else 0.0)
+    no_device_errors()
+
+
+def check_exact_scores(cfg, pg, q, o, b, p0, split):
+    """check_attention for scores that are single products: no error but the cap's."""
+    n = q.shape[0]
+    K, V = pg.dense(b, p0 + n)
+    mask = torch.arange(p0 + n, device="cuda")[None] <= p0 + torch.arange(n, device="cuda")[:, None]
+    for h in range(cfg.q_heads):
+        kv = h // (cfg.q_heads // cfg.kv_heads)
+        want, av, mag = ref.attend(q[:, h].double(), K[kv], V[kv], mask, cfg.c().scale, cfg.c().softcap)
+        bound = ref.attend_bound(want, av, 0 * mag, cfg.head_dim, p0 + n, o.dtype, cfg.softcap, split)
+        # the cap's polynomial: 5.6e-6 of the cap where it is used
+        bound = bound + 2 * 5.6e-6 * min(cfg.softcap, 100.0) * av
+        base.within(o[:, h], want, bound, f"{b} head {h}")
+
+
+# (scale, cap, score over cap): scale / cap down to 1e-10, where its powers
+# leave FP32.
+FAR_CAPS = [(1e-4, 1e6, 0.5), (1e-2, 1e6, 0.7), (0.3, 1e4, 0.6), (1e-3, 1e3, 0.5), (0.125, 50.0, 0.7), (1e-6, 50.0, 0.5)]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("scale,softcap,y", FAR_CAPS)
+def test_equal_capped_scores_weigh_the_same(D, scale, softcap, y):
+    """Two tokens with the same key, opposite values and by far the largest
+    score cancel, also where one stands in a tile with a score outside the
+    reach of the cap's polynomial (far on the other side, without weight)."""
+    g = gen(63)
+    cfg = lq.AttnConfig(2, 1, D, scale=scale, softcap=softcap)
+    n, new = 400, 3
+    pg = Paged(g, cfg, 1, 16, 25)
+    pg.fill(g, [n])
+    pg.k.zero_()
+    qk = y * softcap / scale  # the product of query and key
+    k0 = 2.0 ** (math.floor(math.log2(qk)) // 2)
+    q = torch.zeros(new, 2, D, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = qk / k0
+
+    def put(t, k, v):
+        page = pg.table[0, t // 16].long()
+        pg.k[page, 0, t % 16, 0] = k
+        if v is not None:
+            pg.v[page, 0, t % 16] = v
+    v = randn(g, D, dtype=torch.bfloat16)
+    put(5, k0, v)
+    put(300, k0, -v)
+    put(310, -3 * k0, None)
+    o = torch.empty_like(q)
+    lq.lq_attn_prefill(cfg, pg.cache, torch.full((1,), n - new, dtype=torch.int32, device="cuda"), None, q, o)
+    # Equal products give equal scores where one formula serves both tokens.
+    # Up to a cap of 100 a tile may take the polynomial: its error moves the
+    # weights by 5.6e-6 cap, and they are rounded to 2^-8 of that difference's
+    # neighbourhood of 1.  The other tokens weigh at most n e^(-cap tanh y).
+    rest = n * math.exp(-softcap * math.tanh(0.99 * y))
+    slack = 5.6e-6 * softcap + 2.0 ** -8 if softcap <= 100.0 else 2.0 ** -22
+    bound = (0.5 * slack + 4 * rest) * v.double().abs() + rest * 10
+    assert (o.double().abs() <= bound).all(), f"{o.double().abs().max().item():.2e}"
+    no_device_errors()
