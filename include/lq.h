@@ -539,7 +539,9 @@ LQ_API lq_status lq_attn_decode(const lq_attn_config *cfg, const lq_kv_cache *ca
  * with a position >= max_pages * page_size leaves its row as it is
  * (LQ_DEVERR_BAD_POSITION); bad pages as for lq_attn_decode.  tokens == 0 is
  * a no-op.  One launch.  With io_dtype LQ_BF16 the softmax weights are
- * rounded to BF16 for the product with V.  How a row's keys are shared out
+ * rounded to BF16 for the product with V, and before that are good to 1e-4
+ * (relative); with a softcap of at most 100 scores are good to 5.6e-6 softcap
+ * (larger ones: to the rounding of an FP32 tanh).  How a row's keys are shared out
  * between blocks, and with it the rounding, depends on tokens, batch and
  * max_pages, never on scheduling.
  * Places of the cache that no new token of a sequence sees may hold anything,

@@ -587,17 +587,19 @@ __device__ __forceinline__ void ex2_fma(f32x2 v, float &a, float &b) {
 
 // cap tanh(z x) in units of log2 for |z x| <= 3/4, as x times a polynomial in
 // x^2 whose coefficients hold z and the cap: tanh y = y + y^3 (c0 + c1 y^2 +
-// c2 y^4), least maximum error 5.6e-6.  The coefficients hold powers of z up to
-// the 7th and the cap (1e-3 to 1e6): with z between 2^-14 and 2^14 all of them
-// are normal numbers; other z take capped_log2.
-constexpr float kTanhReach = 0.75f;
+// c2 y^4), least maximum error 5.6e-6.  That error of a score grows with the
+// cap: up to a cap of 100 it moves a weight by 5.6e-4 at most, a seventh of the
+// BF16 rounding that follows.  The coefficients hold powers of z up to the 7th:
+// with z between 2^-14 and 2^14 all of them are normal numbers.  Other caps and
+// other z take capped_log2.
+constexpr float kTanhReach = 0.75f, kPolyCap = 100.0f;
 struct CapPoly {
     float k[4];
 };
 // |x| up to which the polynomial serves (-1: not at all).
-__device__ __forceinline__ float cap_reach(float z) {
+__device__ __forceinline__ float cap_reach(float z, float cap) {
     z = fabsf(z);
-    return z >= 1.0f / 16384.0f && z <= 16384.0f ? kTanhReach / z : -1.0f;
+    return cap <= kPolyCap && z >= 1.0f / 16384.0f && z <= 16384.0f ? kTanhReach / z : -1.0f;
 }
 __device__ __forceinline__ CapPoly cap_poly(float z, float out) {
     const float z3 = z * z * z, z5 = z3 * z * z, z7 = z5 * z * z;
@@ -903,7 +905,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
         const float c = CAP ? 1.0f : fmaxf(fabsf(a.scale * kLog2e), 1e-30f);
         const SoftCap cap = soft_cap(a.scale, a.softcap);
         const CapPoly poly = cap_poly(cap.in, cap.out);
-        const float in_reach = cap_reach(cap.in);
+        const float in_reach = cap_reach(cap.in, a.softcap);
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int j = 0; j < n; ++j) {

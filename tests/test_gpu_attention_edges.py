@@ -72,12 +72,15 @@ def check_exact_scores(cfg, pg, q, o, b, p0, split):
 
 
 # (scale, cap, score over cap): scale / cap down to 1e-10, where its powers
-# leave FP32.
+# leave FP32, and caps of 300 and more, of which 5.6e-6 nears or passes the
+# weights' rounding.
 FAR_CAPS = [(1e-4, 1e6, 0.5), (1e-2, 1e6, 0.7), (0.3, 1e4, 0.6), (1e-3, 1e3, 0.5), (0.125, 50.0, 0.7), (1e-6, 50.0, 0.5)]
+LARGE_CAPS = [(0.125, s, y) for s in (300.0, 1e3) for y in (0.3, 0.5, 0.7)] + \
+    [(scale, s, y) for scale, s in ((2.0, 1e4), (20.0, 1e5), (200.0, 1e6)) for y in (0.1, 0.3, 0.5, 0.7)]
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("scale,softcap,y", FAR_CAPS)
+@pytest.mark.parametrize("scale,softcap,y", FAR_CAPS + LARGE_CAPS)
 def test_equal_capped_scores_weigh_the_same(D, scale, softcap, y):
     """Two tokens with the same key, opposite values and by far the largest
     score cancel, also where one stands in a tile with a score outside the
