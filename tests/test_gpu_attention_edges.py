@@ -116,3 +116,112 @@ def test_equal_capped_scores_weigh_the_same(D, scale, softcap, y):
     bound = (0.5 * slack + 4 * rest) * v.double().abs() + rest * 10
     assert (o.double().abs() <= bound).all(), f"{o.double().abs().max().item():.2e}"
     no_device_errors()
+
+
+# ------------------------------------------------------------------ what an output must not depend on
+
+INDEPENDENT = [
+    # new tokens, starts, Hq, Hkv, D, page, window, softcap, io
+    ([5, 37, 130], [0, 211, 7], 4, 1, 64, 16, 0, 20.0, BF),
+    ([5, 37, 130], [0, 211, 7], 4, 2, 128, 64, 0, 20.0, BF),
+    ([5, 37, 130], [3, 211, 70], 2, 2, 256, 32, 50, 20.0, BF),
+    ([5, 37, 130], [3, 211, 70], 8, 1, 64, 256, 70, 20.0, BF),
+    ([5, 37, 130], [0, 211, 7], 4, 2, 128, 64, 33, 0.0, BF),
+    ([3, 2, 5], [5000, 3, 900], 8, 2, 128, 128, 0, 20.0, BF),
+    ([3, 2, 5], [5000, 3, 900], 4, 2, 64, 32, 700, 20.0, BF),
+]
+
+
+class Independent:
+    """A prefill call whose cache, queries and single places can be changed."""
+
+    def __init__(self, new, start, Hq, Hkv, D, page, window, softcap, io):
+        g = self.g = gen(71 + D)
+        self.cfg = lq.AttnConfig(Hq, Hkv, D, io_dtype=io, window=window, softcap=softcap, scale=D ** -0.5)
+        self.new, self.start = new, start
+        reach = [s + n for s, n in zip(start, new)]
+        self.pg = Paged(g, self.cfg, len(new), page, -(-max(reach) // page) + 1)
+        self.pg.fill(g, reach)
+        self.cu = torch.tensor([0] + torch.tensor(new).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+        self.pos = torch.tensor(start, dtype=torch.int32, device="cuda")
+        self.q = randn(g, sum(new), Hq, D, dtype=DT[io], scale=2.0)
+        # places of the cache that some new token of their sequence sees
+        self.seen = torch.zeros(self.pg.k.shape[:1] + self.pg.k.shape[2:3], dtype=torch.bool, device="cuda")
+        for b, (n, s) in enumerate(zip(new, start)):
+            p = torch.arange(max(0, s + 1 - window) if window else 0, s + n, device="cuda")
+            self.seen[self.pg.table[b].long()[p // page], p % page] = True
+        self.seen = self.seen[:, None, :, None].expand_as(self.pg.k)
+
+    def run(self):
+        o = torch.empty_like(self.q)
+        lq.lq_attn_prefill(self.cfg, self.pg.cache, self.pos, self.cu, self.q, o)
+        return o
+
+    def decode(self):
+        """The last new token of each sequence."""
+        q = self.q[self.cu[1:].long() - 1].contiguous()
+        o = torch.empty_like(q)
+        lq.lq_attn_decode(self.cfg, self.pg.cache, self.pos + torch.tensor(self.new, device="cuda", dtype=torch.int32) - 1, q, o)
+        return o
+
+
+ANYTHING = [math.nan, 3e38, -3e38, math.inf, 7.0]
+
+
+@pytest.mark.parametrize("case", INDEPENDENT)
+def test_outputs_do_not_depend_on_places_that_no_token_sees(case):
+    c = Independent(*case)
+    for x in (c.pg.k, c.pg.v):
+        x[~c.seen] = 0.0
+    want, want_d = c.run(), c.decode()
+    for b, s in enumerate(c.start):
+        rows = slice(int(c.cu[b]), int(c.cu[b + 1]))
+        check_attention(c.cfg, c.pg, c.q[rows], want[rows], b, s, split_of(c.cfg.io_dtype), f"sequence {b}")
+    for fill in ANYTHING:
+        for x in (c.pg.k, c.pg.v):
+            x[~c.seen] = fill
+        assert torch.equal(c.run(), want), f"prefill: {fill} in places that no token sees"
+        assert torch.equal(c.decode(), want_d), f"decode: {fill} in places that no token sees"
+    no_device_errors()
+
+
+@pytest.mark.parametrize("case", INDEPENDENT)
+def test_outputs_do_not_depend_on_later_tokens(case):
+    """Another key, value and query of a sequence's last new token leave the
+    outputs of those before it as they are, to the bit."""
+    c = Independent(*case)
+    want = c.run()
+    last = (c.cu[1:] - 1).long()
+    before = torch.ones(c.q.shape[0], dtype=torch.bool, device="cuda")
+    before[last] = False
+    page = c.pg.page
+    for size in (30.0, 3000.0, 1e-3):
+        for b, (n, s) in enumerate(zip(c.new, c.start)):
+            p = s + n - 1
+            at = (c.pg.table[b, p // page].long(), slice(None), p % page)
+            for x in (c.pg.k, c.pg.v):
+                x[at] = randn(c.g, *x[at].shape, dtype=x.dtype, scale=size)
+        c.q[last] = randn(c.g, *c.q[last].shape, dtype=c.q.dtype, scale=size)
+        assert torch.equal(c.run()[before], want[before]), f"size {size}"
+    no_device_errors()
+
+
+@pytest.mark.parametrize("case", INDEPENDENT)
+def test_outputs_do_not_depend_on_other_sequences(case):
+    """Other queries, keys and values of one sequence, NaN among them, leave
+    the outputs of the others as they are, to the bit."""
+    c = Independent(*case)
+    want = c.run()
+    for b in range(len(c.new)):
+        rows = torch.zeros(c.q.shape[0], dtype=torch.bool, device="cuda")
+        rows[int(c.cu[b]):int(c.cu[b + 1])] = True
+        q, pages = c.q.clone(), c.pg.table[b].long()
+        k, v = c.pg.k[pages].clone(), c.pg.v[pages].clone()
+        for size in (1e-3, 3000.0, math.nan):
+            c.q[rows] = randn(c.g, *c.q[rows].shape, dtype=c.q.dtype, scale=size)
+            c.pg.k[pages] = randn(c.g, *k.shape, dtype=k.dtype, scale=size)
+            c.pg.v[pages] = randn(c.g, *v.shape, dtype=v.dtype, scale=size)
+            assert torch.equal(c.run()[~rows], want[~rows]), f"sequence {b}, size {size}"
+        c.q.copy_(q)
+        c.pg.k[pages], c.pg.v[pages] = k, v
+    no_device_errors()
