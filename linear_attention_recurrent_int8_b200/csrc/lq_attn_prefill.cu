@@ -226,9 +226,9 @@ __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
     __syncthreads();
 
     const SoftCap cap = soft_cap(a.scale, a.softcap);
-    int pos[2];  // of rows g and g + 8
-    for (int r = 0; r < 2; ++r) pos[r] = p0 + ((16 * rg + g + 8 * r) >> group_shift);
-    const int pw0 = p0 + ((16 * rg) >> group_shift), pw1 = p0 + ((16 * rg + 15) >> group_shift);
+    int pos[2];  // of rows g and g + 8 (rows past the last token see what it sees, no further keys)
+    for (int r = 0; r < 2; ++r) pos[r] = min(p0 + ((16 * rg + g + 8 * r) >> group_shift), len - 1);
+    const int pw0 = min(p0 + ((16 * rg) >> group_shift), len - 1), pw1 = min(p0 + ((16 * rg + 15) >> group_shift), len - 1);
     const float *qr = qs + (16 * rg + g) * LD;
     float o[NB][4][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll

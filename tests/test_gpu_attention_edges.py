@@ -129,6 +129,10 @@ INDEPENDENT = [
     ([5, 37, 130], [0, 211, 7], 4, 2, 128, 64, 33, 0.0, BF),
     ([3, 2, 5], [5000, 3, 900], 8, 2, 128, 128, 0, 20.0, BF),
     ([3, 2, 5], [5000, 3, 900], 4, 2, 64, 32, 700, 20.0, BF),
+    ([5, 37, 130], [0, 211, 7], 4, 1, 64, 16, 0, 20.0, F32),
+    ([5, 37, 130], [0, 211, 7], 3, 3, 128, 64, 0, 0.0, F32),
+    ([5, 37, 130], [3, 211, 70], 8, 2, 256, 32, 50, 0.0, F32),
+    ([3, 2, 5], [5000, 3, 900], 8, 2, 128, 128, 0, 20.0, F32),
 ]
 
 
