@@ -408,8 +408,9 @@ struct F32Core {
                 odd = odd || (seen[n][e] && s[n][e] != s[n][e]);
             }
         if (__any_sync(0xffffffffu, odd)) {
-            // The split turns an infinity into NaN: such a tile's scores are
-            // formed again, in FP32.
+            // The split turns an infinity into NaN: such scores (and no
+            // others, of whatever heads share the warp) are formed again, in
+            // FP32.
             const float *qp = static_cast<const float *>(a.q) + ((size_t)b * a.Hq + head0 + g) * D;
 #pragma unroll 1
             for (int i = 0; i < 2 * NT && g < rows; ++i) {
@@ -423,7 +424,7 @@ struct F32Core {
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        if (2 * n + e == i) s[n][e] = x;
+                        if (2 * n + e == i && s[n][e] != s[n][e]) s[n][e] = x;
             }
             __syncwarp();
         }

@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
 #pragma unroll
             for (int e = 0; e < 4; ++e) odd = odd || (s[k][e] != s[k][e] && seen(e >> 1, k, e & 1));
         if (__any_sync(0xffffffffu, odd)) {
-            // The split turns an infinity into NaN: such a tile's scores are
-            // formed again, in FP32.
+            // The split turns an infinity into NaN: such scores (and no
+            // others, of whatever rows share the warp) are formed again, in FP32.
 #pragma unroll 1
             for (int i = 0; i < 4 * NT; ++i) {
                 const int tok = 8 * (i >> 2) + 2 * t + (i & 1);
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
                 for (int k = 0; k < NT; ++k)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (4 * k + e == i) s[k][e] = v;
+                        if (4 * k + e == i && s[k][e] != s[k][e]) s[k][e] = v;
             }
         }
         if constexpr (NBUF == 1) {

@@ -207,6 +207,42 @@ def test_outputs_do_not_depend_on_later_tokens(case):
                 x[at] = randn(c.g, *x[at].shape, dtype=x.dtype, scale=size)
         c.q[last] = randn(c.g, *c.q[last].shape, dtype=c.q.dtype, scale=size)
         assert torch.equal(c.run()[before], want[before]), f"size {size}"
+    # infinite keys and queries (a value that a row does not see has to be finite)
+    for b, (n, s) in enumerate(zip(c.new, c.start)):
+        p = s + n - 1
+        c.pg.k[c.pg.table[b, p // page].long(), :, p % page, ::3] = math.inf
+        c.pg.v[c.pg.table[b, p // page].long(), :, p % page] = 0.5
+    c.q[last, :, 1::5] = -math.inf
+    assert torch.equal(c.run()[before], want[before]), "infinite"
+    no_device_errors()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,io", [(4, 1, 64, F32), (20, 2, 128, F32), (6, 2, 256, F32), (8, 1, 128, BF), (40, 2, 64, BF)])
+def test_heads_do_not_depend_on_each_other(Hq, Hkv, D, io):
+    """Infinite or NaN queries of one head leave the outputs of the others as
+    they are, to the bit."""
+    g = gen(73)
+    cfg = lq.AttnConfig(Hq, Hkv, D, io_dtype=io)
+    lens = [777, 1, 3000]
+    pg = Paged(g, cfg, 3, 32, 100)
+    pg.fill(g, lens)
+    q = randn(g, 3, Hq, D, dtype=DT[io], scale=2.0)
+    pos = torch.tensor(lens, dtype=torch.int32, device="cuda") - 1
+
+    def run():
+        od, op = torch.empty_like(q), torch.empty_like(q)
+        lq.lq_attn_decode(cfg, pg.cache, pos, q, od)
+        lq.lq_attn_prefill(cfg, pg.cache, pos, None, q, op)
+        return od, op
+    want = run()
+    for h in range(Hq):
+        others = torch.arange(Hq, device="cuda") != h
+        keep = q[:, h].clone()
+        for x in (math.inf, math.nan):
+            q[:, h, 3::7] = x
+            for got, w in zip(run(), want):
+                assert torch.equal(got[:, others], w[:, others]), f"head {h}, {x}"
+        q[:, h] = keep
     no_device_errors()
 
 
