@@ -63,6 +63,24 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
     }
 }
 
+// The same for a converged warp, with one outcome for all of its lanes: each
+// lane reads the clock for itself, and warp-wide instructions follow a wait.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+    bool done = bar_test(bar, parity);
+    if (!__all_sync(0xffffffffu, done)) {
+        const unsigned long long t0 = global_ns();
+        int k = 0;
+        do {
+            done = bar_test(bar, parity);
+            if ((++k & 31) == 0 && __any_sync(0xffffffffu, global_ns() - t0 > kWaitLimitNs)) {
+                atomicOr(&g_dev_error, kErrWaitTimeout);
+                return false;
+            }
+        } while (!__all_sync(0xffffffffu, done));
+    }
+    return true;
+}
+
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;

@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
         };
         // tile j of K or V into the next slot
         auto load = [&](const CUtensorMap *map, int j, int z, bool is_v) {
-            if (use > 0 && !bar_wait(&bars.kv_empty[slot], (use - 1) & 1)) return false;
+            if (use > 0 && !warp_wait(&bars.kv_empty[slot], (use - 1) & 1)) return false;
             unsigned char *dst = ring + slot * T::kSlotBytes;
             const int k0 = (k_first + j) * KT;
             // V rows that no query row sees may hold NaN, which a weight of
@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
                 tma_page_load(dst + x * (KT * 128) + bx * box_rows * 128, map, 64 * x,
                               (k0 + bx * box_rows) & (a.page_size - 1), z, bar);
             if (clear) {
-                if (!bar_wait(&bars.tail, tail_phase)) return false;
+                if (!warp_wait(&bars.tail, tail_phase)) return false;
                 tail_phase ^= 1;
                 for (int i = lane; i < KT * D / 8; i += 32) {
                     const int r = i / (D / 8), c = i - r * (D / 8);
@@ -807,9 +807,9 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
         int slot = 0, use = 0;
         auto take = [&](int &at) {
             at = slot;
-            const bool ok = bar_wait(&bars.kv_full[slot], use & 1);
+            const bool ok = warp_wait(&bars.kv_full[slot], use & 1);
             if (++slot == T::kSlots) slot = 0, ++use;
-            return __all_sync(0xffffffffu, ok) != 0;
+            return ok;
         };
         // scores of one stream into its score tile at column col: the tile's
         // last weights were read by an earlier MMA of this thread
@@ -829,9 +829,8 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
                 mma_ts(tm + T::kColO + s * D, col + 8 * k, v_desc + k * (2048 / 16), id_pv, add || i > 0);
             }
         };
-        auto wait = [&](uint64_t *bar, int parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity)) != 0; };
         int ks = 0, vs = 0;
-        bool ok = n > 0 && wait(&bars.q_full, 0) && take(ks);
+        bool ok = n > 0 && warp_wait(&bars.q_full, 0) && take(ks);
         tc_fence_after_sync();
         if (ok && elect_one()) {
 #pragma unroll
@@ -869,12 +868,12 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
             }
             for (int s = 0; ok && s < streams; ++s) {
                 const uint32_t col = tm + T::kColS + (T::kTiles == 2 ? 2 * s + (j & 1) : s) * KT;
-                ok = wait(&bars.p_half[s], j & 1);
+                ok = warp_wait(&bars.p_half[s], j & 1);
                 if (!ok) break;
                 tc_fence_after_sync();
                 if (elect_one()) pv(s, vs, col, 0, j > 0);
                 __syncwarp();
-                ok = wait(&bars.p_ready[s], j & 1);
+                ok = warp_wait(&bars.p_ready[s], j & 1);
                 if (!ok) break;
                 tc_fence_after_sync();
                 if (elect_one()) {
@@ -911,7 +910,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
         for (int j = 0; j < n; ++j) {
             const int buf = T::kTiles == 2 ? 2 * s + (j & 1) : s;
             const uint32_t sa = lanes + T::kColS + buf * KT;
-            if (!bar_wait(&bars.s_full[buf], T::kTiles == 2 ? (j >> 1) & 1 : j & 1)) { ok = false; break; }
+            if (!warp_wait(&bars.s_full[buf], T::kTiles == 2 ? (j >> 1) & 1 : j & 1)) { ok = false; break; }
             tc_fence_after_sync();
             float x[KT];
             tmem_load_row(sa, x);
@@ -986,7 +985,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
                 if (j > 0) {
                     // (with one score tile, these scores followed that product)
                     if (T::kTiles == 2) {
-                        if (!bar_wait(&bars.o_done[s], (j - 1) & 1)) { ok = false; break; }
+                        if (!warp_wait(&bars.o_done[s], (j - 1) & 1)) { ok = false; break; }
                         tc_fence_after_sync();
                     }
 #pragma unroll 1
@@ -1004,7 +1003,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
             f32x2 sum0 = two(0.0f, 0.0f), sum1 = sum0;
             // with two score tiles, the barriers' phase of the tile before
             // must have been passed before they are arrived at again
-            if (T::kTiles == 2 && j > 0 && !bar_wait(&bars.o_done[s], (j - 1) & 1)) { ok = false; break; }
+            if (T::kTiles == 2 && j > 0 && !warp_wait(&bars.o_done[s], (j - 1) & 1)) { ok = false; break; }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 constexpr int HW = KT / 4;  // words of half a tile's weights
@@ -1037,7 +1036,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
             apart(add2(sum0, sum1), sa0, sb0);
             l += sa0 + sb0;
         }
-        ok = ok && (n == 0 || bar_wait(&bars.o_done[s], T::kTiles == 2 ? (n - 1) & 1 : 0));
+        ok = ok && (n == 0 || warp_wait(&bars.o_done[s], T::kTiles == 2 ? (n - 1) & 1 : 0));
         tc_fence_after_sync();
         if (split > 1) {
             // all products are done with the operands once every stream is
