@@ -411,8 +411,10 @@ __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
     }
-    // join the two halves of the keys: group 1 hands over through shared memory
-    __syncthreads();
+    // Join the groups' parts of the keys, which groups 1 and up hand over
+    // through shared memory.  With one of the waits out of time the block's
+    // rows are not valid: they are left out or, in a split call, NaN.
+    ok = __syncthreads_and(ok);
     const int split = split_of_tile;
     constexpr int JLD = D + 2;
     float *jo = reinterpret_cast<float *>(ring) + rg * 16 * JLD;
@@ -431,8 +433,6 @@ __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
     }
     __syncthreads();
     if (kg == 0) {
-        // (out of time: NaN, which reaches the output of a split call)
-        if (!ok) m[0] = m[1] = NAN;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int R = 16 * rg + g + 8 * r, tok = R >> group_shift;

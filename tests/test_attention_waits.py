@@ -22,3 +22,14 @@ def test_an_expired_wait_has_one_outcome_for_the_warp(name):
     s = source(name)
     assert not re.findall(r"!\s*bar_wait\(", s)
     assert s.count("warp_wait(") > 0
+
+
+def test_a_key_group_out_of_time_counts_for_the_block():
+    """FP32 prefill: the groups of a block hold parts of the same rows' keys,
+    so that the rows are not valid when any group gave up."""
+    s = source("lq_attn_prefill.cu")
+    body = s[s.index("attn_prefill_f32(const"):s.index("int group_shift_of(")]
+    loop_end = body.index("mbar_arrive(&empty[kg][1][buf])")
+    joined = body.index("ok = __syncthreads_and(ok);")
+    assert loop_end < joined < body.index("JLD")  # before the parts are handed over
+    assert "dst[D] = ok ? top : NAN" in body[joined:] and "if (split == 1 && !ok) continue;" in body[joined:]
