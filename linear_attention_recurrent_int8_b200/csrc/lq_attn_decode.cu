@@ -647,10 +647,11 @@ __global__ void __launch_bounds__(Tile<D, BF16>::kWarps * 32, 1)
     for (int i = 0; i < run; ++i) {
         if (fresh) begin();
         if (!warp_wait(full + st, ph)) {
-            // give the copies still in flight their time before the block's shared memory is freed
-            for (int k = i + 1; k < filled; ++k) {
-                if (++st == pl.stages) st = 0, ph ^= 1;
+            // give the copies in flight (this one again) their time before the
+            // block's shared memory is freed
+            for (int k = i; k < filled; ++k) {
                 bar_wait(full + st, ph);
+                if (++st == pl.stages) st = 0, ph ^= 1;
             }
             return;
         }

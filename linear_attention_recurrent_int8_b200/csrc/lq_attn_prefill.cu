@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
     float *qs = reinterpret_cast<float *>(ring + 2 * KG * NBUF * T::kHalfBytes);
     __shared__ uint64_t full[KG][2][2], empty[KG][2][2];  // [key group][K (and V with two buffers), V][buffer]
     __shared__ int find[T::kThreads / 32 + 6];
+    __shared__ int sent[KG][2];  // tiles whose copies were issued, by the barrier they arrive at
     const BlockPlace at = place_of(a, group_shift, cluster);
     const QueryTile qt = find_query_tile<T::kThreads, (T::kBlocks > 1)>(a, T::kRows >> group_shift, at.turn, at.tiles, find);
     if (qt.rows <= 0) return;
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
         const int k0 = (k_first + KG * i + kg) * KT;
         uint64_t *bar = &full[kg][v][i % NBUF];
         unsigned char *kdst = ring + (2 * kg * NBUF + i % NBUF) * T::kHalfBytes, *vdst = kdst + NBUF * T::kHalfBytes;
+        sent[kg][v] = i + 1;
         mbar_arrive_expect_tx(bar, NBUF > 1 ? 2 * T::kHalfBytes : T::kHalfBytes);
         for (int r = 0; r < KT; r += 16) {
             const int tok = k0 + r;
@@ -238,7 +240,8 @@ __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[x][i][e] = 0.0f;
     bool ok = true;
-    for (int it = 0; it < mine; ++it) {
+    int it = 0;
+    for (; it < mine; ++it) {
         const int k0 = (k_first + KG * it + kg) * KT;
         const int buf = it % NBUF, phase = it / NBUF & 1;
         const unsigned char *kbuf = ring + (2 * kg * NBUF + buf) * T::kHalfBytes;
@@ -411,6 +414,9 @@ __global__ void __launch_bounds__(F32<D, KG>::kThreads, F32<D, KG>::kBlocks)
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
     }
+    // out of time: copies still in flight get theirs before the ring takes the parts
+    for (int v = 0; !ok && producer && v < (NBUF > 1 ? 1 : 2); ++v)
+        for (int i = it; i < sent[kg][v]; ++i) bar_wait(&full[kg][v][i % NBUF], i / NBUF & 1);
     // Join the groups' parts of the keys, which groups 1 and up hand over
     // through shared memory.  With one of the waits out of time the block's
     // rows are not valid: they are left out or, in a split call, NaN.
@@ -672,7 +678,7 @@ struct Tc {
 };
 
 struct TcBars {
-    uint64_t q_full, kv_full[5], kv_empty[5], s_full[2], p_half[2], p_ready[2], o_done[2], tail;
+    uint64_t q_full, kv_full[5], kv_empty[5], s_full[2], p_half[2], p_ready[2], o_done[2], tail, all_done;
 };
 
 // One block: 128 kStreams rows, each a (token, head) pair of `group` heads
@@ -725,6 +731,9 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem_slot, 0);
+    // the parts of a split call go in the operands' place: every warp passes
+    // here once its copies and products are done
+    auto operands_free = [] { asm volatile("bar.sync 1, %0;" ::"n"(T::kThreads) : "memory"); };
 
     if (warp == T::kLoadWarp) {
         // ------------------------------------------------------------ TMA
@@ -770,7 +779,10 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
                 tma_page_load(dst + x * (KT * 128) + bx * box_rows * 128, map, 64 * x,
                               (k0 + bx * box_rows) & (a.page_size - 1), z, bar);
             if (clear) {
-                if (!warp_wait(&bars.tail, tail_phase)) return false;
+                if (!warp_wait(&bars.tail, tail_phase)) {
+                    bar_wait(&bars.tail, tail_phase);  // (as below)
+                    return false;
+                }
                 tail_phase ^= 1;
                 for (int i = lane; i < KT * D / 8; i += 32) {
                     const int r = i / (D / 8), c = i - r * (D / 8);
@@ -796,6 +808,13 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
                 ok = load(&kmap, j + 1, z, false);
             }
             if (ok && T::kTiles == 2) ok = load(&vmap, j, zv, true);
+        }
+        // Whoever gave up, the copies land (or get their time) before this
+        // memory takes the parts of a split call or is freed.
+        if (n > 0) {
+            bar_wait(&bars.q_full, 0);
+            const int fills = use * T::kSlots + slot;
+            for (int i = max(0, fills - T::kSlots); i < fills; ++i) bar_wait(&bars.kv_full[i % T::kSlots], i / T::kSlots & 1);
         }
     } else if (warp == T::kMmaWarp) {
         // ------------------------------------------------------------ MMAs
@@ -888,6 +907,12 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
                 }
                 __syncwarp();
             }
+        }
+        // the products issued so far as well
+        if (n > 0) {
+            if (elect_one()) mma_commit(&bars.all_done);
+            __syncwarp();
+            bar_wait(&bars.all_done, 0);
         }
     } else if (warp < 4 * streams) {
         // ------------------------------------------------------------ softmax: one row per thread
@@ -1039,9 +1064,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
         ok = ok && (n == 0 || warp_wait(&bars.o_done[s], T::kTiles == 2 ? (n - 1) & 1 : 0));
         tc_fence_after_sync();
         if (split > 1) {
-            // all products are done with the operands once every stream is
-            // here: the parts go in their place
-            asm volatile("bar.sync 1, %0;" ::"r"(128 * streams) : "memory");
+            operands_free();
             float *row = reinterpret_cast<float *>(qs) + R * (D + 4);
 #pragma unroll 1
             for (int k = 0; k < D; k += 16) {
@@ -1079,6 +1102,7 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
     }
     if (split > 1) {
         __syncwarp();
+        if (warp >= 4 * streams) operands_free();
         join_split<D, true>(smem_u32(qs), qt.rows << group_shift, group_shift, split, rank, a, qt, h0);
     }
     tc_fence_before_sync();

@@ -33,3 +33,28 @@ def test_a_key_group_out_of_time_counts_for_the_block():
     joined = body.index("ok = __syncthreads_and(ok);")
     assert loop_end < joined < body.index("JLD")  # before the parts are handed over
     assert "dst[D] = ok ? top : NAN" in body[joined:] and "if (split == 1 && !ok) continue;" in body[joined:]
+
+
+def test_copies_and_products_in_flight_outlive_no_block():
+    """Before a block hands its shared memory on, or leaves it and its TMEM,
+    whoever issued copies or products has waited for them, whatever the waits
+    before returned."""
+    decode = source("lq_attn_decode.cu")
+    gave_up = decode[decode.index("if (!warp_wait(full + st, ph)) {"):]
+    gave_up = gave_up[:gave_up.index("return;")]
+    assert "for (int k = i; k < filled; ++k)" in gave_up and "bar_wait(full + st, ph)" in gave_up
+
+    s = source("lq_attn_prefill.cu")
+    f32 = s[s.index("attn_prefill_f32(const"):s.index("int group_shift_of(")]
+    drain = f32.index("for (int i = it; i < sent[kg][v]; ++i) bar_wait(&full[kg][v][i % NBUF], i / NBUF & 1);")
+    assert f32.index("mbar_arrive(&empty[kg][1][buf])") < drain < f32.index("__syncthreads_and(ok)")
+
+    tc = s[s.index("attn_prefill_tc(const"):]
+    load, rest = tc[tc.index("if (warp == T::kLoadWarp) {"):].split("} else if (warp == T::kMmaWarp) {")
+    products, softmax = rest.split("} else if (warp < 4 * streams) {")
+    assert "bar_wait(&bars.q_full, 0)" in load and "for (int i = max(0, fills - T::kSlots); i < fills; ++i) bar_wait(" in load
+    last = products.rindex("mma_commit(")
+    assert "all_done" in products[last:] and "bar_wait(&bars.all_done, 0)" in products[last:]
+    # the parts of a split call are written after every warp has passed there
+    assert softmax.index("operands_free()") < softmax.index("row[D] =")
+    assert "if (warp >= 4 * streams) operands_free();" in softmax
