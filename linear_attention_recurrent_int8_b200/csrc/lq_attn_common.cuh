@@ -65,20 +65,11 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity) {
 
 // The same for a converged warp, with one outcome for all of its lanes: each
 // lane reads the clock for itself, and warp-wide instructions follow a wait.
+// (A vote after every test instead: BF16 prefill at head size 64, 2 x 4,096
+// tokens behind 4,096, 537 against 502 us.)
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
-    bool done = bar_test(bar, parity);
-    if (!__all_sync(0xffffffffu, done)) {
-        const unsigned long long t0 = global_ns();
-        int k = 0;
-        do {
-            done = bar_test(bar, parity);
-            if ((++k & 31) == 0 && __any_sync(0xffffffffu, global_ns() - t0 > kWaitLimitNs)) {
-                atomicOr(&g_dev_error, kErrWaitTimeout);
-                return false;
-            }
-        } while (!__all_sync(0xffffffffu, done));
-    }
-    return true;
+    if (__all_sync(0xffffffffu, bar_test(bar, parity))) return true;
+    return __all_sync(0xffffffffu, bar_wait(bar, parity)) != 0;
 }
 
 // One lane of the (converged) warp.
