@@ -265,3 +265,110 @@ def test_outputs_do_not_depend_on_other_sequences(case):
         c.q.copy_(q)
         c.pg.k[pages], c.pg.v[pages] = k, v
     no_device_errors()
+
+
+# ------------------------------------------------------------------ every key once
+
+def check_weights_of_pages(cfg, pg, o, b, p0):
+    """Outputs for queries of zeros over values that are 1 in one channel, by
+    the token's group of 16: channel c is the share of the visible tokens whose
+    group is c modulo the head size.  Weights of 1, sums of whole numbers and a
+    power of two per part are exact, so the reciprocal of the sum (2 half steps
+    of FP32), a product and the output's rounding are all the error there is:
+    one token more or less in a group, or a group left out, is far above it."""
+    n = o.shape[0]
+    for i in range(n):
+        p = p0 + i
+        lo = max(0, p + 1 - cfg.window) if cfg.window else 0
+        t = torch.arange(lo, p + 1, device="cuda")
+        want = torch.bincount(t // 16 % cfg.head_dim, minlength=cfg.head_dim).double() / len(t)
+        bound = (ref.HALF[o.dtype] + 4 * 2.0 ** -24) * want
+        base.within(o[i], want.expand(cfg.q_heads, -1), bound, f"sequence {b}, position {p}")
+
+
+def pages_by_group(cfg, g, lens, page):
+    """A cache whose values are the groups' indicators; keys are random."""
+    pg = Paged(g, cfg, len(lens), page, -(-max(lens) // page))
+    pg.fill(g, lens)
+    for b, n in enumerate(lens):
+        t = torch.arange(n, device="cuda")
+        v = torch.zeros(n, cfg.kv_heads, cfg.head_dim, dtype=cfg.io_torch_dtype, device="cuda")
+        v[t, :, t // 16 % cfg.head_dim] = 1.0
+        pg.v[pg.table[b].long()[t // page], :, t % page] = v
+    return pg
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new,start,Hq,Hkv,page,window", [
+    # one sequence: the keys of a tile split over up to 8 blocks
+    ([1], [127], 2, 1, 16, 0), ([1], [128], 2, 1, 16, 0), ([2], [255], 2, 1, 64, 0), ([1], [320], 4, 1, 16, 0),
+    ([3], [511], 2, 1, 32, 0), ([2], [1022], 8, 2, 16, 0), ([5], [2000], 2, 2, 128, 0), ([2], [5119], 4, 1, 256, 0),
+    ([3], [20011], 4, 2, 64, 0), ([2], [6000], 2, 1, 16, 1000), ([4], [6000], 2, 1, 32, 4097),
+    # several, of very different lengths
+    ([1, 3, 2], [9000, 17, 300], 2, 1, 16, 0), ([2, 1, 4, 1], [700, 0, 1300, 260], 4, 4, 64, 0),
+    ([4, 9], [3000, 130], 2, 1, 32, 129),
+    # longer runs: tiles of many rows
+    ([70, 33], [200, 1000], 8, 1, 64, 0), ([300], [77], 4, 1, 16, 100),
+])
+def test_prefill_takes_every_key_once(new, start, Hq, Hkv, page, window, D, io):
+    g = gen(81)
+    cfg = lq.AttnConfig(Hq, Hkv, D, io_dtype=io, window=window)
+    lens = [s + n for s, n in zip(start, new)]
+    pg = pages_by_group(cfg, g, lens, page)
+    cu = torch.tensor([0] + torch.tensor(new).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    q = torch.zeros(sum(new), Hq, D, dtype=DT[io], device="cuda")
+    o = torch.full_like(q, 3.0)
+    lq.lq_attn_prefill(cfg, pg.cache, torch.tensor(start, dtype=torch.int32, device="cuda"), cu, q, o)
+    for b, s in enumerate(start):
+        check_weights_of_pages(cfg, pg, o[int(cu[b]):int(cu[b + 1])], b, s)
+    no_device_errors()
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,Hq,Hkv,page,window", [
+    ([1, 15, 16, 17, 31, 32, 33, 500], 2, 1, 16, 0),
+    ([1, 15, 16, 17, 31, 32, 33, 500], 6, 2, 32, 17),
+    ([20011], 4, 2, 64, 0), ([6000, 1, 900], 2, 2, 16, 1000),
+    ([2500, 40], 24, 1, 128, 0), ([3000, 800, 17], 40, 1, 16, 0), ([900, 2000], 33, 1, 64, 700),
+])
+def test_decode_takes_every_key_once(lens, Hq, Hkv, page, window, D, io):
+    g = gen(82)
+    cfg = lq.AttnConfig(Hq, Hkv, D, io_dtype=io, window=window)
+    pg = pages_by_group(cfg, g, lens, page)
+    q = torch.zeros(len(lens), Hq, D, dtype=DT[io], device="cuda")
+    o = torch.full_like(q, 3.0)
+    lq.lq_attn_decode(cfg, pg.cache, torch.tensor(lens, dtype=torch.int32, device="cuda") - 1, q, o)
+    for b, n in enumerate(lens):
+        check_weights_of_pages(cfg, pg, o[b:b + 1], b, n - 1)
+    no_device_errors()
+
+
+# ------------------------------------------------------------------ decode: row groups and joins
+
+@pytest.mark.parametrize("pos,Hq,Hkv,D,page,window,softcap,io", [
+    # FP32 with 2 and 3 row groups of 8 to a key-value head, BF16 with 3 of 16
+    ([900, 17, 401], 16, 1, 128, 16, 0, 0.0, F32),
+    ([900, 17, -1, 401], 40, 2, 64, 32, 0, 0.0, F32),
+    ([900, 17, 401], 20, 1, 256, 64, 100, 20.0, F32),
+    ([900, 17, 401], 40, 1, 128, 16, 0, 0.0, BF),
+    ([5000, 0], 33, 1, 64, 64, 0, 0.0, BF),
+    ([30000, 12], 80, 2, 256, 128, 0, 30.0, BF),
+    ([30000], 20, 1, 64, 16, 0, 0.0, F32),
+    # more row groups than warps of a block
+    ([700, 90], 160, 1, 64, 16, 0, 0.0, BF),
+    ([700, 90], 100, 1, 128, 16, 0, 0.0, F32),
+])
+def test_decode_row_groups(pos, Hq, Hkv, D, page, window, softcap, io):
+    base.test_decode(pos, Hq, Hkv, D, page, window, softcap, io)
+
+
+@pytest.mark.parametrize("D,Hkv,io", [(64, 2, BF), (128, 1, BF), (256, 2, BF), (64, 2, F32), (128, 4, F32)])
+def test_decode_of_few_long_among_many_short_sequences(D, Hkv, io):
+    """Enough heads for blocks that join 8 of them, some with more parts than a
+    warp joins alone."""
+    g = gen(83)
+    pos = torch.randint(-1, 100, (60,), generator=g, device="cuda").tolist()
+    pos[7], pos[44] = 30000, 17011
+    base.test_decode(pos, 32, Hkv, D, 64, 0, 0.0, io)
