@@ -20,6 +20,12 @@ _current_device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
+def _check_i32(value, name: str):
+    """ctypes would cut the value off to 32 bits."""
+    if not -(1 << 31) <= value < 1 << 31:
+        raise ValueError(f"{name}: {value} is not a 32-bit integer")
+
+
 @dataclass(frozen=True)
 class AttnConfig:
     """lq_attn_config.  ``scale`` defaults to head_dim ** -0.5."""
@@ -36,10 +42,14 @@ class AttnConfig:
     window: int = 0
 
     def __post_init__(self):
+        for name in ("q_heads", "kv_heads", "head_dim", "io_dtype", "norm", "rot_dim", "rot_pairs", "window"):
+            _check_i32(getattr(self, name), name)
         scale = self.head_dim ** -0.5 if self.scale is None and self.head_dim > 0 else self.scale
         c = _lq.LqAttnConfig(self.q_heads, self.kv_heads, self.head_dim, self.io_dtype, self.norm,
                              self.rot_dim, self.rot_pairs, self.window, self.eps, scale or 0.0,
                              self.softcap)
+        if c.softcap == 0.0 and self.softcap != 0.0:  # (0 would mean no cap)
+            raise ValueError(f"softcap: {self.softcap} is below the range of float")
         object.__setattr__(self, "_c", c)
         object.__setattr__(self, "_ref", ctypes.byref(c))
         object.__setattr__(self, "_layout", (self.kv_heads, self.head_dim, self.io_dtype))
@@ -75,6 +85,8 @@ class KvCache:
         self.device = k_pages.device
         self.batch, self.max_pages = block_table.shape
         self.num_pages, _, self.page_size, _ = k_pages.shape
+        for name in ("batch", "max_pages", "num_pages", "page_size"):
+            _check_i32(getattr(self, name), name)
         self._c = _lq.LqKvCache(k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
                                 self.batch, self.num_pages, self.page_size, self.max_pages)
         self._ref = ctypes.byref(self._c)
@@ -289,6 +301,7 @@ def lq_kv_append(cfg: AttnConfig, cache: KvCache, pos, cu_tokens, q, k, v, q_wei
 def lq_attn_workspace_bytes(cfg: AttnConfig, batch: int) -> int:
     """Bytes of lq_attn_decode's workspace on the current device; -1 for an
     invalid configuration or batch."""
+    _check_i32(batch, "batch")
     return _lq.load_library().lq_attn_workspace_bytes(cfg._ref, int(batch))
 
 

@@ -288,3 +288,18 @@ def test_scales_and_caps_out_of_range_are_refused(change):
 def test_the_smallest_eps():
     assert norm_call(cfg_c(norm=lq.LQ_NORM_L2, eps=1e-31)) == INVALID
     assert norm_call(cfg_c(norm=lq.LQ_NORM_L2, eps=1e-30), tokens=0) == OK
+
+
+@pytest.mark.parametrize("change", [dict(window=1 << 32), dict(window=(1 << 32) + 5), dict(window=1 << 63), dict(q_heads=(1 << 32) + 8),
+                                    dict(rot_dim=1 << 40), dict(norm=(1 << 32) + 1), dict(softcap=1e-60)])
+def test_values_past_the_fields_of_the_struct_are_refused(change):
+    """A window of 2^32 would be cut off to 0, which is none; so would a cap
+    below the range of float."""
+    with pytest.raises(ValueError, match=next(iter(change))):
+        lq.AttnConfig(**{**dict(q_heads=8, kv_heads=2), **change})
+    with pytest.raises(ValueError, match="batch"):
+        lq.lq_attn_workspace_bytes(lq.AttnConfig(8, 2), (1 << 32) + 4)
+    assert lq.AttnConfig(8, 2, window=(1 << 31) - 1).c().window == (1 << 31) - 1
+    kp = torch.empty(1, 2, 16, 128, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="max_pages"):
+        lq.KvCache(lq.AttnConfig(8, 2), kp, kp, torch.empty(1, (1 << 32) + 4, dtype=torch.int32, device="meta"))
