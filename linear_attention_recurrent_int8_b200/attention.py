@@ -211,7 +211,7 @@ def _check_places(cache: KvCache, pos, cu_tokens, tokens: int):
     _check_vector(pos, "pos", _i32, cache.batch)
     if cu_tokens is not None:
         _check_vector(cu_tokens, "cu_tokens", _i32, cache.batch + 1)
-    elif tokens % cache.batch != 0:
+    elif cache.batch < 1 or tokens % cache.batch != 0:
         raise ValueError(f"{tokens} tokens for {cache.batch} sequences need cu_tokens")
 
 
@@ -336,7 +336,7 @@ def lq_attn_prefill(cfg: AttnConfig, cache: KvCache, pos, cu_tokens, q, o, strea
     head_dim]; pos and cu_tokens as for lq_kv_append."""
     _check_cache(cfg, cache)
     _check_dense(q, "q", cfg.io_torch_dtype)
-    n = q.numel() // (cfg.q_heads * cfg.head_dim)
+    n = q.numel() // max(cfg.q_heads * cfg.head_dim, 1)  # (the library refuses heads of none)
     _check_out(q, "q", cfg, n, cfg.q_heads)
     _check_out(o, "o", cfg, n, cfg.q_heads)
     _check_places(cache, pos, cu_tokens, n)

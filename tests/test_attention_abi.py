@@ -303,3 +303,17 @@ def test_values_past_the_fields_of_the_struct_are_refused(change):
     kp = torch.empty(1, 2, 16, 128, dtype=torch.bfloat16, device="meta")
     with pytest.raises(ValueError, match="max_pages"):
         lq.KvCache(lq.AttnConfig(8, 2), kp, kp, torch.empty(1, (1 << 32) + 4, dtype=torch.int32, device="meta"))
+
+
+def test_calls_without_sequences_or_heads_are_refused():
+    cfg = lq.AttnConfig(4, 2, 64)
+    kp = zeros(9, 2, 16, 64)
+    none = lq.KvCache(cfg, kp, kp.clone(), zeros(0, 5, dtype=torch.int32))
+    q, k, pos = zeros(6, 4, 64), zeros(6, 2, 64), zeros(0, dtype=torch.int32)
+    with pytest.raises(ValueError, match="0 sequences"):
+        lq.lq_kv_append(cfg, none, pos, None, None, k, k, None, None, None, None)
+    with pytest.raises(ValueError, match="0 sequences"):
+        lq.lq_attn_prefill(cfg, none, pos, None, q, q)
+    some = lq.KvCache(cfg, kp, kp.clone(), zeros(3, 5, dtype=torch.int32))
+    with pytest.raises(ValueError, match="q: shape"):
+        lq.lq_attn_prefill(lq.AttnConfig(0, 2, 64), some, zeros(3, dtype=torch.int32), None, q, q)
