@@ -543,7 +543,9 @@ LQ_API lq_status lq_attn_decode(const lq_attn_config *cfg, const lq_kv_cache *ca
  * (relative); with a softcap of at most 100 scores are good to 5.6e-6 softcap
  * (larger ones: to the rounding of an FP32 tanh).  How a row's keys are
  * shared out between blocks, and with it the rounding, depends on tokens,
- * batch and max_pages, never on scheduling.
+ * batch, max_pages, pos and cu_tokens, never on scheduling; apart from that a
+ * token's output depends on nothing that the token does not see (but for the
+ * last sentence here).
  * Places of the cache that no new token of a sequence sees may hold anything,
  * NaN included.  A NaN or infinite value v that some of a sequence's new
  * tokens see may also reach outputs of its others (their weight for it is

@@ -14,12 +14,18 @@
 // and its keys are read once for all of its heads.
 //
 // Measured on B200 (cuBLAS BF16 burst 1,645 TFLOP/s): 2 x 4,096 tokens behind
-// 4,096, 32 query and 8 key-value heads, BF16: 676 us at head size 128 (1,220
-// TFLOP/s; tensor pipe 58 %, special function unit 51 %: neither waits for
-// the other but for the hand-over of scores and weights), 504 us at 64 (the
-// exponentials: one per 256 operations).  FP32, 2 x 2,048 behind 2,048, 16
-// and 4 heads: 2.11 ms at head size 128, 49 TFLOP/s, half of what three warp
-// MMAs per product allow.
+// 4,096, 32 query and 8 key-value heads, BF16: 681 us at head size 128 (1,210
+// TFLOP/s; tensor pipe 59 %, special function unit 52 %: neither waits for
+// the other but for the hand-over of scores and weights), 502 us at 64 (the
+// exponentials: one per 256 operations); 16 and 2 heads at 256: 714 us (1,155
+// TFLOP/s, tensor pipe 55 %).  FP32, 2 x 2,048 behind 2,048, 16 and 4 heads:
+// 2.06 ms at head size 128, 50 TFLOP/s, half of what three warp MMAs per
+// product allow.
+//
+// Weights enter the BF16 product with V rounded to BF16, the tensor cores'
+// operand type (2^-8 relative at most; their sum is of the unrounded ones):
+// outputs are 2.3e-3 off the 64-bit ones, against 1.7e-3 for weights in FP32,
+// which is the output's own rounding.
 #include <algorithm>
 
 #include "lq_attn_common.cuh"
@@ -951,9 +957,9 @@ __global__ void __launch_bounds__(Tc<D, NS>::kThreads, Tc<D, NS>::kBlocks)
                 // of the warp is outside, those that a row does not see are
                 // cleared and its others looked at again.  (Rows that differ
                 // take both ways in turn: 2 x 2,048 tokens behind 2,048, cap
-                // 50, scores of 15 on average, 485 us at head size 64 and 569
-                // at 128, against 412 and 490 with one choice for the warp;
-                // scores of 1, 215 and 245 against 210 and 244.)
+                // 50, scores around 15, 490 us at head size 64 and 573 at 128,
+                // against 413 and 489 with one choice for the warp; scores
+                // around 1, 215 and 246 against 210 and 245.)
                 auto inside = [&] {
                     float big0 = 0.0f, big1 = 0.0f;
 #pragma unroll

@@ -16,8 +16,9 @@
 // Measured on B200 (6.55 TB/s copy): 16,384 tokens of 32 + 32 heads, head size
 // 128, BF16, L2 norm: 80 us, 6.6 TB/s of algorithmic traffic.  9,458 ragged
 // tokens of 16 + 2 + 2 heads at head size 256, RMS norm, rotation, appended:
-// 45 us, 4.3 TB/s; there instruction issue bounds it (65 % of the slots:
-// conversions, norm and rotation of 8 channels are about 40 instructions).
+// 45 us, 4.3 TB/s; issue takes 65 % of the slots there (conversions, norm and
+// rotation of 8 channels are about 40 instructions) and the L1 data pipe 59 %
+// (a row's weights are loaded with it).
 // Two tokens: 2.1 us.  Lanes of 16 channels (52 us appended), several tokens
 // to a block (46 to 72) and a shared-memory ring filled by bulk copies (57)
 // were slower.
