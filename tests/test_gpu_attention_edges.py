@@ -1,6 +1,7 @@
 """The softmax-attention operators at the ends of their ranges, and what their
 outputs must not depend on."""
 import math
+import threading
 
 import pytest
 import torch
@@ -372,3 +373,70 @@ def test_decode_of_few_long_among_many_short_sequences(D, Hkv, io):
     pos = torch.randint(-1, 100, (60,), generator=g, device="cuda").tolist()
     pos[7], pos[44] = 30000, 17011
     base.test_decode(pos, 32, Hkv, D, 64, 0, 0.0, io)
+
+
+# ------------------------------------------------------------------ calls at once
+
+def test_graphs_at_once_and_calls_from_threads():
+    """A layer's step of several configurations: graphs of it replayed at once
+    on streams of their own, and calls from as many host threads, give what
+    the calls give alone (workspaces allocated by the calls)."""
+    steps, outs, streams = [], [], []
+    for i, (D, io) in enumerate([(64, BF), (128, BF), (256, BF), (64, F32), (128, F32), (256, F32), (64, BF)]):
+        g = gen(90 + i)
+        cfg = lq.AttnConfig(8, 2, D, io_dtype=io, norm=lq.LQ_NORM_RMS, rot_dim=D // 2, softcap=30.0 if i % 2 else 0.0)
+        pg = Paged(g, cfg, 3, 64, 40)
+        pg.fill(g, [2001, 4, 701])
+        pos = torch.tensor([2000, 3, 700], dtype=torch.int32, device="cuda")
+        qkv = randn(g, 3, 12 * D, dtype=DT[io])
+        w, cs = 1 + 0.2 * randn(g, D), ref.table(D // 2, 40 * 64).cuda()
+        qo, od, op = (torch.zeros(3, 8, D, dtype=DT[io], device="cuda") for _ in range(3))
+
+        def step(cfg=cfg, pg=pg, pos=pos, qkv=qkv, w=w, cs=cs, qo=qo, od=od, op=op, D=D):
+            q, k, v = (qkv[:, a * D:b * D].view(3, -1, D) for a, b in ((0, 8), (8, 10), (10, 12)))
+            lq.lq_kv_append(cfg, pg.cache, pos, None, q, k, v, w, w, cs, qo)
+            lq.lq_attn_decode(cfg, pg.cache, pos, qo, od)
+            lq.lq_attn_prefill(cfg, pg.cache, pos, None, qo, op)
+        steps.append(step)
+        outs.append((qo, od, op))
+        streams.append(torch.cuda.Stream())
+    for step in steps:
+        step()
+    torch.cuda.synchronize()
+    alone = [[x.clone() for x in xs] for xs in outs]
+
+    def check(what):
+        torch.cuda.synchronize()
+        for i, (xs, ys) in enumerate(zip(outs, alone)):
+            assert all(torch.equal(x, y) for x, y in zip(xs, ys)), f"{what}, configuration {i}"
+            for x in xs:
+                x.zero_()
+        torch.cuda.synchronize()
+
+    check("alone")
+    graphs = [torch.cuda.CUDAGraph() for _ in steps]
+    for graph, step in zip(graphs, steps):
+        with torch.cuda.graph(graph):
+            step()
+    for _ in range(20):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    check("graphs at once")
+    failed = []
+
+    def work(step, stream):
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(50):
+                    step()
+        except Exception as e:  # for the assertion below: a thread's exception ends nothing else
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=a) for a in zip(steps, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    check("threads")
+    no_device_errors()
